@@ -35,8 +35,9 @@
  *   - Alignment: every device pointer must be 16-byte aligned (d_count and d_idx: 4).
  *     Leading dimensions only need to cover a row, except where a call copies rows
  *     with 16-byte bulk or tensor copies: the ldx of every decode and prefill call
- *     (spw_spmv and its group, FFN, no-alloc, tensor-core and auto forms; spw_spmm,
- *     spw_spmm_tokens, spw_spmm24, spw_group_tokens) must be a multiple of 8 fp16
+ *     (spw_spmv and its group, FFN, no-alloc, tensor-core, auto and epilogue forms;
+ *     spw_spmm, spw_spmm_tokens, spw_spmm24, spw_group_tokens; spw_spmm_ep, spw_spmm_ffn
+ *     and the two backward calls, with spw_spmm_backward's lddy) must be a multiple of 8 fp16
  *     elements unless that operand has a single row.  Such copies
  *     may read an activation row up to the next 16-byte boundary past its last
  *     element (never across it, so never outside the row's allocation granule).
@@ -464,6 +465,107 @@ uint64_t spw_spmv_auto_workspace_bytes(const spw_format* hdr, int B);
 int spw_spmv_auto(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, int B, int ldx,
                   float threshold, const uint32_t* d_act_bits, uint16_t* d_y, int ldy, void* d_ws,
                   uint64_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ epilogues
+ * What follows a linear layer's product in a transformer, done in the product's own
+ * kernel (the pages stop at the product; their FFN listing, "Reduced Matrix
+ * Multiplication" §4.2, applies the activation to it):
+ *   out = act(product + bias) + residual
+ * from the fp32 product, with one rounding to fp16 at the end.  bias: N fp16, or NULL.
+ * residual: rows of N fp16 at ldr >= N, or NULL; it may be the output itself (same
+ * pointer and leading dimension), but must not overlap it otherwise.  act, with v the
+ * fp32 sum:
+ *   SPW_ACT_NONE       v
+ *   SPW_ACT_RELU       max(v, 0)
+ *   SPW_ACT_SILU       v / (1 + e^-v)
+ *   SPW_ACT_GELU       v (1 + erf(v / sqrt 2)) / 2
+ *   SPW_ACT_GELU_TANH  v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2
+ * NaN stays NaN; an infinite v gives what the formula gives (SiLU(-Inf) is NaN).  The
+ * struct is read on the host during the call; NULL stands for no bias, no activation and
+ * no residual.  Both pointers 16-byte aligned. */
+typedef enum {
+    SPW_ACT_NONE = 0,
+    SPW_ACT_RELU = 1,
+    SPW_ACT_SILU = 2,
+    SPW_ACT_GELU = 3,
+    SPW_ACT_GELU_TANH = 4
+} spw_activation;
+typedef struct {
+    const uint16_t* bias;
+    const uint16_t* residual;
+    int32_t ldr;
+    int32_t act; /* spw_activation */
+} spw_epilogue;
+
+/* Decode with an epilogue, for 1 to 16 rows: the product is spw_spmv's (same threshold
+ * rule, column set, workspace and its rules, determinism; a dropped weight or column
+ * never touches the sum), the epilogue as above.  Asynchronous.  Errors: as spw_spmv,
+ * plus INVALID_ARG (unknown act, ldr < N) and ALIGNMENT for the epilogue's pointers. */
+int spw_spmv_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, int B, int ldx,
+                float threshold, const uint32_t* d_act_bits, const spw_epilogue* ep, uint16_t* d_y,
+                int ldy, void* d_ws, uint64_t ws_bytes, void* stream);
+
+/* Prefill with an epilogue: Y = act(X W_masked^T + bias) + residual for M rows.  The
+ * weight is expanded to dense fp16 in the workspace and multiplied on tcgen05 SM pairs,
+ * so the workspace is at least 2 N K bytes (rows and columns rounded up to 64).  A
+ * dropped weight is an explicit zero there, so a non-finite X entry reaches every column
+ * of its row, as in spw_spmm.  M >= 0 (M == 0 does nothing).
+ * Workspace of this call and of the three below: spw_..._workspace_bytes(..., M) bytes,
+ * 16-byte aligned, of any content; nothing is kept in it between calls.  Calls that may run
+ * at the same time must not share one.  Deterministic.  Asynchronous.  Errors: INVALID_ARG,
+ * ALIGNMENT, FORMAT, BUFFER_TOO_SMALL, UNSUPPORTED (too many tiles), CUDA; device timeouts
+ * as for spw_spmv.  A tile that disagrees with its header counts as empty (FORMAT through
+ * spw_last_device_status). */
+uint64_t spw_spmm_ep_workspace_bytes(const spw_format* hdr, int M);
+int spw_spmm_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_X, int M, int ldx,
+                const spw_epilogue* ep, uint16_t* d_Y, int ldy, void* d_ws, uint64_t ws_bytes,
+                void* stream);
+
+/* Prefill of the gated block ("Reduced Matrix Multiplication" §4.2 in Llama's gated form;
+ * spw_spmv_ffn is the decode's): both projections, the activation and the product in one
+ * kernel,
+ *   G = X W_gate^T, U = X W_up^T, H = act(G) * U   (M x N, from the fp32 G and U)
+ * each result rounded to fp16 once.  (spw_spmv_ffn rounds g and u before it multiplies.)
+ *   hdr_gate, hdr_up: same N and K.  act: spw_activation; SiLU is Llama's.
+ *   d_G, d_U: M x N at ldg and ldu >= N, written for a backward pass; both NULL otherwise.
+ * Workspace, non-finite entries, M and errors as spw_spmm_ep (both weights expanded). */
+uint64_t spw_spmm_ffn_workspace_bytes(const spw_format* hdr_gate, const spw_format* hdr_up, int M);
+int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_format* hdr_up,
+                 const void* d_buf_up, const uint16_t* d_X, int M, int ldx, int act, uint16_t* d_H,
+                 int ldh, uint16_t* d_G, int ldg, uint16_t* d_U, int ldu, void* d_ws,
+                 uint64_t ws_bytes, void* stream);
+
+/* Gradients of spw_spmm_ffn with the patterns held fixed (fine-tuning of the kept
+ * weights), from X, the G and U it wrote, and dH:
+ *   dG = dH * U * act'(G), dU = dH * act(G)         (M x N, rounded to fp16)
+ *   dX = dG W_gate + dU W_up                        (M x K at lddx >= K)
+ *   dV_gate, dV_up: dG^T X and dU^T X at the kept positions.
+ * The gradient of a kept weight stands where the weight stands in the TCB values section:
+ * dV has (bytes_total - off_values) / 2 fp16 entries (layout above; the filling of a tile
+ * is written as zeros), so an optimiser can update the section in place.
+ *   d_dX may be NULL, and d_dV_gate and d_dV_up (both, and then d_X too); not all of them.
+ *   dX and dV must not overlap any input.  ReLU's slope at 0 is 0.
+ * fp32 sums, one rounding to fp16 of each result; a dG, dU or result beyond fp16 becomes
+ * an infinity, which a loss scaler looks for.  M == 0 writes zeros to dV.  Workspace and
+ * errors as spw_spmm_ep (both weights expanded, dG and dU). */
+uint64_t spw_spmm_ffn_backward_workspace_bytes(const spw_format* hdr_gate, const spw_format* hdr_up,
+                                               int M);
+int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate,
+                          const spw_format* hdr_up, const void* d_buf_up, const uint16_t* d_X, int M,
+                          int ldx, int act, const uint16_t* d_G, int ldg, const uint16_t* d_U, int ldu,
+                          const uint16_t* d_dH, int lddh, uint16_t* d_dX, int lddx,
+                          uint16_t* d_dV_gate, uint16_t* d_dV_up, void* d_ws, uint64_t ws_bytes,
+                          void* stream);
+
+/* Gradients of the plain product Y = X W_masked^T (spw_spmm; spw_spmm_ep without an
+ * activation), the pattern held fixed:  dX = dY W_masked  (M x K) and dV = dY^T X at the
+ * kept positions, packed as above.  dY: M x N at lddy, a multiple of 8 unless M == 1.
+ * d_dX or d_dV (and with it d_X) may be NULL, not both.  M == 0 writes zeros to dV.
+ * Workspace and errors as spw_spmm_ep. */
+uint64_t spw_spmm_backward_workspace_bytes(const spw_format* hdr, int M);
+int spw_spmm_backward(const spw_format* hdr, const void* d_buf, const uint16_t* d_X, int M, int ldx,
+                      const uint16_t* d_dY, int lddy, uint16_t* d_dX, int lddx, uint16_t* d_dV,
+                      void* d_ws, uint64_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then read and clear the library's device status word for the
  * current device: *code = SPW_OK, SPW_ERR_TIMEOUT if a bounded device wait ran out, or

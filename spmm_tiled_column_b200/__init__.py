@@ -27,6 +27,15 @@ SPW_ERR_UNSUPPORTED = 5
 SPW_ERR_CUDA = 6
 SPW_ERR_TIMEOUT = 7
 
+# Activations of the epilogues and of the gated block, by number or by name
+SPW_ACT_NONE = 0
+SPW_ACT_RELU = 1
+SPW_ACT_SILU = 2
+SPW_ACT_GELU = 3
+SPW_ACT_GELU_TANH = 4
+ACTIVATIONS = {"none": SPW_ACT_NONE, "relu": SPW_ACT_RELU, "silu": SPW_ACT_SILU,
+               "gelu": SPW_ACT_GELU, "gelu_tanh": SPW_ACT_GELU_TANH}
+
 # C function name -> (argtypes, restype)
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -58,6 +67,15 @@ class spw_spmm_plan_info(ctypes.Structure):
                 ("whole_tiles", ctypes.c_int32), ("ctas", ctypes.c_int32),
                 ("cta_pair", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("workspace_bytes", ctypes.c_uint64)]
+
+
+class spw_epilogue(ctypes.Structure):
+    """bias, residual (with its leading dimension) and activation of a product's epilogue."""
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("ldr", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
+_EP = ctypes.POINTER(spw_epilogue)
 SIGNATURES = {
     "spw_status_string": ([_I], ctypes.c_char_p),
     "spw_version": ([], _I),
@@ -97,6 +115,16 @@ SIGNATURES = {
     "spw_spmm24_workspace_bytes": ([_FP, _I], _U64),
     "spw_spmm24_plan": ([_FP, _I, _I, ctypes.POINTER(spw_spmm_plan_info)], _I),
     "spw_spmm24": ([_FP, _P, _P, _U64, _P, _I, _I, _P, _I, _P, _U64, _P], _I),
+    "spw_spmv_ep": ([_FP, _P, _P, _I, _I, _F, _P, _EP, _P, _I, _P, _U64, _P], _I),
+    "spw_spmm_ep_workspace_bytes": ([_FP, _I], _U64),
+    "spw_spmm_ep": ([_FP, _P, _P, _I, _I, _EP, _P, _I, _P, _U64, _P], _I),
+    "spw_spmm_ffn_workspace_bytes": ([_FP, _FP, _I], _U64),
+    "spw_spmm_ffn": ([_FP, _P, _FP, _P, _P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _U64, _P], _I),
+    "spw_spmm_ffn_backward_workspace_bytes": ([_FP, _FP, _I], _U64),
+    "spw_spmm_ffn_backward": ([_FP, _P, _FP, _P, _P, _I, _I, _I, _P, _I, _P, _I, _P, _I, _P, _I, _P, _P,
+                               _P, _U64, _P], _I),
+    "spw_spmm_backward_workspace_bytes": ([_FP, _I], _U64),
+    "spw_spmm_backward": ([_FP, _P, _P, _I, _I, _P, _I, _P, _I, _P, _P, _U64, _P], _I),
 }
 
 
@@ -736,6 +764,244 @@ def spw_spmm24(hdr_r, buf_r: torch.Tensor, s24: torch.Tensor, X: torch.Tensor,
     return Y
 
 
+# ------------------------------------------------------------------ epilogues, gated block, gradients
+
+def _act(act) -> int:
+    """An activation's number from its number or name."""
+    if isinstance(act, str):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
+        return ACTIVATIONS[act]
+    return int(act)
+
+
+def _same_device(first: torch.Tensor, **tensors):
+    """The library works on the current device: every tensor has to live there."""
+    dev = torch.cuda.current_device()
+    for name, t in {"the input": first, **tensors}.items():
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            raise ValueError(f"{name} is on {t.device}; the current CUDA device is cuda:{dev}")
+
+
+def _out(t: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, name: str):
+    """An fp16 output of at least rows x cols (allocated when not given): (tensor, view, ld)."""
+    if t is None:
+        t = torch.empty((rows, cols), dtype=torch.float16, device=like.device)
+    v, ld = _rows(_half(t, name), name)
+    _need(v, rows, cols, name)
+    return t, v, ld
+
+
+def _in(t: torch.Tensor, rows: int, cols: int, name: str):
+    """An fp16 operand of exactly rows x cols: (view, ld)."""
+    v, ld = _rows(_half(t, name), name)
+    if tuple(v.shape) != (rows, cols):
+        raise ValueError(f"{name} is {tuple(v.shape)}; the call takes {rows} x {cols}")
+    return v, ld
+
+
+def _x_of(x: torch.Tensor, K: int, name: str):
+    """Rows of activations of exactly K columns: (view, rows, ld)."""
+    v, ld = _rows(_half(x, name), name)
+    if v.shape[1] != K:
+        raise ValueError(f"{name} has {v.shape[1]} columns; the weight has {K}")
+    return v, v.shape[0], ld
+
+
+def _values_len(h) -> int:
+    return int(h.bytes_total - h.off_values) // 2
+
+
+def _packed(t: torch.Tensor | None, h, like: torch.Tensor, name: str) -> torch.Tensor:
+    """A packed gradient: one fp16 entry for each entry of the values section."""
+    n = _values_len(h)
+    if t is None:
+        return torch.empty(n, dtype=torch.float16, device=like.device)
+    t = _half(t, name)
+    if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1) or t.numel() < n:
+        raise ValueError(f"{name} must be 1-D and contiguous with at least {n} entries")
+    return t
+
+
+def _packed_ptr(dv: torch.Tensor | None, ws: torch.Tensor):
+    """The pointer of a packed gradient.  That of a weight with nothing kept is empty, and an
+    empty tensor has no address: any aligned one stands for it, nothing is written there."""
+    return _ptr(ws) if dv is not None and dv.numel() == 0 else _ptr(dv)
+
+
+def _ws_of(ws: torch.Tensor | None, need: int, like: torch.Tensor) -> torch.Tensor:
+    return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device) if ws is None else ws
+
+
+def _epilogue(bias, act, residual, rows: int, N: int) -> spw_epilogue:
+    ep = spw_epilogue(None, None, 0, _act(act))
+    if bias is not None:
+        b = _half(bias, "bias")
+        if b.dim() != 1 or b.numel() != N or (N > 1 and b.stride(0) != 1):
+            raise ValueError(f"bias must be 1-D and contiguous with {N} entries, got {tuple(b.shape)}")
+        ep.bias = b.data_ptr()
+    if residual is not None:
+        r, ep.ldr = _in(residual, rows, N, "residual")
+        ep.residual = r.data_ptr()
+    return ep
+
+
+def spw_spmv_ep(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
+                act_bits: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                act=SPW_ACT_NONE, residual: torch.Tensor | None = None,
+                y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Decode with an epilogue: y = act(W_masked . x~ + bias) + residual (B x N fp16, B <= 16).
+
+    bias: N fp16; residual: B x N fp16 (it may be y itself); act: a name of ACTIVATIONS or its
+    number; the rest as spw_spmv, whose workspace this call uses."""
+    h = _hdr(hdr)
+    x2, B, ldx = _x_of(x, h.K, "x")
+    _same_device(x, buf=buf, act_bits=act_bits, bias=bias, residual=residual, y=y, ws=ws)
+    ep = _epilogue(bias, act, residual, B, h.N)
+    _need_buf(buf, h)
+    _need_words(act_bits, h.K)
+    y, y2, ldy = _out(y, B, h.N, x, "y")
+    if ws is None:
+        ws = torch.zeros(max(spw_spmv_workspace_bytes(h, B), 16), dtype=torch.uint8, device=x.device)
+    _check("spw_spmv_ep", lib().spw_spmv_ep(
+        ctypes.byref(h), _ptr(buf), _ptr(x2), B, ldx, float(threshold), _ptr(act_bits),
+        ctypes.byref(ep), _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream(stream)))
+    return y
+
+
+def spw_spmm_ep_workspace_bytes(hdr, M: int) -> int:
+    return int(lib().spw_spmm_ep_workspace_bytes(ctypes.byref(_hdr(hdr)), int(M)))
+
+
+def spw_spmm_ep(hdr, buf: torch.Tensor, X: torch.Tensor, bias: torch.Tensor | None = None,
+                act=SPW_ACT_NONE, residual: torch.Tensor | None = None,
+                Y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Prefill with an epilogue: Y = act(X . W_masked^T + bias) + residual (M x N fp16).
+
+    bias, act and residual as spw_spmv_ep.  ws: spw_spmm_ep_workspace_bytes(hdr, M) bytes of
+    any content (allocated here when not given)."""
+    h = _hdr(hdr)
+    X2, M, ldx = _x_of(X, h.K, "X")
+    _same_device(X, buf=buf, bias=bias, residual=residual, Y=Y, ws=ws)
+    ep = _epilogue(bias, act, residual, M, h.N)
+    _need_buf(buf, h)
+    Y, Y2, ldy = _out(Y, M, h.N, X, "Y")
+    ws = _ws_of(ws, spw_spmm_ep_workspace_bytes(h, M), X)
+    _check("spw_spmm_ep", lib().spw_spmm_ep(
+        ctypes.byref(h), _ptr(buf), _ptr(X2), M, ldx, ctypes.byref(ep), _ptr(Y2), ldy, _ptr(ws),
+        _nbytes(ws), _stream(stream)))
+    return Y
+
+
+def spw_spmm_ffn_workspace_bytes(hdr_gate, hdr_up, M: int) -> int:
+    return int(lib().spw_spmm_ffn_workspace_bytes(ctypes.byref(_hdr(hdr_gate)),
+                                                  ctypes.byref(_hdr(hdr_up)), int(M)))
+
+
+def spw_spmm_ffn(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor, X: torch.Tensor,
+                 act=SPW_ACT_SILU, save: bool = False, H: torch.Tensor | None = None,
+                 G: torch.Tensor | None = None, U: torch.Tensor | None = None,
+                 ws: torch.Tensor | None = None, stream=None):
+    """Prefill of the gated block in one kernel: H = act(X . W_gate^T) * (X . W_up^T), M x N.
+
+    Returns H, or (H, G, U) with the two projections when save is set or G and U are given
+    (what spw_spmm_ffn_backward takes).  ws: spw_spmm_ffn_workspace_bytes(...) bytes."""
+    hg, hu = _hdr(hdr_gate), _hdr(hdr_up)
+    X2, M, ldx = _x_of(X, hg.K, "X")
+    if (G is None) != (U is None):
+        raise ValueError("G and U go together")
+    save = save or G is not None
+    _same_device(X, buf_gate=buf_gate, buf_up=buf_up, H=H, G=G, U=U, ws=ws)
+    _need_buf(buf_gate, hg, "buf_gate")
+    _need_buf(buf_up, hu, "buf_up")
+    H, H2, ldh = _out(H, M, hg.N, X, "H")
+    G2 = U2 = None
+    ldg = ldu = 0
+    if save:
+        G, G2, ldg = _out(G, M, hg.N, X, "G")
+        U, U2, ldu = _out(U, M, hg.N, X, "U")
+    ws = _ws_of(ws, spw_spmm_ffn_workspace_bytes(hg, hu, M), X)
+    _check("spw_spmm_ffn", lib().spw_spmm_ffn(
+        ctypes.byref(hg), _ptr(buf_gate), ctypes.byref(hu), _ptr(buf_up), _ptr(X2), M, ldx, _act(act),
+        _ptr(H2), ldh, _ptr(G2), ldg, _ptr(U2), ldu, _ptr(ws), _nbytes(ws), _stream(stream)))
+    return (H, G, U) if save else H
+
+
+def spw_spmm_ffn_backward_workspace_bytes(hdr_gate, hdr_up, M: int) -> int:
+    return int(lib().spw_spmm_ffn_backward_workspace_bytes(
+        ctypes.byref(_hdr(hdr_gate)), ctypes.byref(_hdr(hdr_up)), int(M)))
+
+
+def spw_spmm_ffn_backward(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor,
+                          X: torch.Tensor | None, G: torch.Tensor, U: torch.Tensor, dH: torch.Tensor,
+                          act=SPW_ACT_SILU, need_dx: bool = True, need_dv: bool = True,
+                          dX: torch.Tensor | None = None, dV_gate: torch.Tensor | None = None,
+                          dV_up: torch.Tensor | None = None, ws: torch.Tensor | None = None,
+                          stream=None):
+    """Gradients of spw_spmm_ffn, the patterns held fixed: (dX, dV_gate, dV_up).
+
+    dV_*: the kept weights' gradients in the order of the buffers' values sections (1-D fp16).
+    need_dx / need_dv False leaves that part out (None in its place; X may then be None for
+    need_dv False).  ws: spw_spmm_ffn_backward_workspace_bytes(...) bytes."""
+    hg, hu = _hdr(hdr_gate), _hdr(hdr_up)
+    G2, ldg = _rows(_half(G, "G"), "G")
+    M = G2.shape[0]
+    _in(G, M, hg.N, "G")
+    U2, ldu = _in(U, M, hg.N, "U")
+    dH2, lddh = _in(dH, M, hg.N, "dH")
+    if need_dv and X is None:
+        raise ValueError("the weights' gradients need X")
+    X2, ldx = _in(X, M, hg.K, "X") if X is not None else (None, 0)
+    _same_device(G, U=U, dH=dH, X=X, buf_gate=buf_gate, buf_up=buf_up, dX=dX, dV_gate=dV_gate,
+                 dV_up=dV_up, ws=ws)
+    _need_buf(buf_gate, hg, "buf_gate")
+    _need_buf(buf_up, hu, "buf_up")
+    dX2, lddx = None, 0
+    if need_dx:
+        dX, dX2, lddx = _out(dX, M, hg.K, G, "dX")
+    else:
+        dX = None
+    dV_gate = _packed(dV_gate, hg, G, "dV_gate") if need_dv else None
+    dV_up = _packed(dV_up, hu, G, "dV_up") if need_dv else None
+    ws = _ws_of(ws, spw_spmm_ffn_backward_workspace_bytes(hg, hu, M), G)
+    _check("spw_spmm_ffn_backward", lib().spw_spmm_ffn_backward(
+        ctypes.byref(hg), _ptr(buf_gate), ctypes.byref(hu), _ptr(buf_up), _ptr(X2), M, ldx, _act(act),
+        _ptr(G2), ldg, _ptr(U2), ldu, _ptr(dH2), lddh, _ptr(dX2), lddx, _packed_ptr(dV_gate, ws),
+        _packed_ptr(dV_up, ws), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return dX, dV_gate, dV_up
+
+
+def spw_spmm_backward_workspace_bytes(hdr, M: int) -> int:
+    return int(lib().spw_spmm_backward_workspace_bytes(ctypes.byref(_hdr(hdr)), int(M)))
+
+
+def spw_spmm_backward(hdr, buf: torch.Tensor, X: torch.Tensor | None, dY: torch.Tensor,
+                      need_dx: bool = True, need_dv: bool = True, dX: torch.Tensor | None = None,
+                      dV: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Gradients of Y = X . W_masked^T, the pattern held fixed: (dX, dV); dV, need_* and X as
+    spw_spmm_ffn_backward.  ws: spw_spmm_backward_workspace_bytes(hdr, M) bytes."""
+    h = _hdr(hdr)
+    dY2, M, lddy = _x_of(dY, h.N, "dY")
+    if need_dv and X is None:
+        raise ValueError("the weight's gradient needs X")
+    X2, ldx = _in(X, M, h.K, "X") if X is not None else (None, 0)
+    _same_device(dY, X=X, buf=buf, dX=dX, dV=dV, ws=ws)
+    _need_buf(buf, h)
+    dX2, lddx = None, 0
+    if need_dx:
+        dX, dX2, lddx = _out(dX, M, h.K, dY, "dX")
+    else:
+        dX = None
+    dV = _packed(dV, h, dY, "dV") if need_dv else None
+    ws = _ws_of(ws, spw_spmm_backward_workspace_bytes(h, M), dY)
+    _check("spw_spmm_backward", lib().spw_spmm_backward(
+        ctypes.byref(h), _ptr(buf), _ptr(X2), M, ldx, _ptr(dY2), lddy, _ptr(dX2), lddx,
+        _packed_ptr(dV, ws), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return dX, dV
+
+
 class SparseLinear24:
     """A weight held as its 2:4 part (sparse tensor cores) plus a TCB residual: a holder
     for spw_split24, spw_compress and spw_spmm24 (it adds no arithmetic)."""
@@ -784,5 +1050,53 @@ class SparseLinear:
     def spmm_tokens(self, X, threshold=0.0, Y=None, ws=None, stream=None):
         return spw_spmm_tokens(self.hdr, self.buf, X, threshold, Y, ws, stream=stream)
 
+    def spmv_ep(self, x, threshold=0.0, act_bits=None, bias=None, act=SPW_ACT_NONE, residual=None,
+                y=None, stream=None):
+        x2 = x if x.dim() == 2 else x.unsqueeze(0)
+        return spw_spmv_ep(self.hdr, self.buf, x2, threshold, act_bits, bias, act, residual, y,
+                           self.workspace(x2.shape[0]), stream)
+
+    def spmm_ep(self, X, bias=None, act=SPW_ACT_NONE, residual=None, Y=None, ws=None, stream=None):
+        return spw_spmm_ep(self.hdr, self.buf, X, bias, act, residual, Y, ws, stream)
+
+    def spmm_backward(self, X, dY, need_dx=True, need_dv=True, ws=None, stream=None):
+        return spw_spmm_backward(self.hdr, self.buf, X, dY, need_dx, need_dv, ws=ws, stream=stream)
+
+    def values(self) -> torch.Tensor:
+        """The kept weights as they stand in the buffer (fp16 view of the values section, the
+        order of a packed gradient; a tile's filling must stay zero)."""
+        return self.buf[self.hdr.off_values:self.hdr.bytes_total].view(torch.float16)
+
     def decompress(self, out=None, stream=None):
         return spw_decompress(self.hdr, self.buf, out, stream)
+
+
+class SparseFFN:
+    """The gate and up projections of a gated block with its activation (a holder for the
+    calls above; it adds no arithmetic): spmv for 1 to 16 tokens, spmm for more, backward."""
+
+    def __init__(self, gate: SparseLinear, up: SparseLinear, act=SPW_ACT_SILU):
+        if (gate.N, gate.K) != (up.N, up.K):
+            raise ValueError(f"gate is {gate.N} x {gate.K}, up {up.N} x {up.K}")
+        self.gate, self.up, self.act = gate, up, _act(act)
+        self._ws = {}
+
+    def spmv(self, x, threshold=0.0, h=None, act_bits=None, stream=None):
+        """(h, column-set words) of the decode's fused step (SiLU only)."""
+        if self.act != SPW_ACT_SILU:
+            raise ValueError("the decode form computes SiLU")
+        x2 = x if x.dim() == 2 else x.unsqueeze(0)
+        B = x2.shape[0]
+        if B not in self._ws:
+            need = spw_spmv_ffn_workspace_bytes(self.gate.hdr, self.up.hdr, B)
+            self._ws[B] = torch.zeros(max(need, 16), dtype=torch.uint8, device=self.gate.buf.device)
+        return spw_spmv_ffn(self.gate.hdr, self.gate.buf, self.up.hdr, self.up.buf, x2, threshold, h,
+                            act_bits, self._ws[B], stream)
+
+    def spmm(self, X, save=False, H=None, G=None, U=None, ws=None, stream=None):
+        return spw_spmm_ffn(self.gate.hdr, self.gate.buf, self.up.hdr, self.up.buf, X, self.act, save,
+                            H, G, U, ws, stream)
+
+    def backward(self, X, G, U, dH, need_dx=True, need_dv=True, ws=None, stream=None):
+        return spw_spmm_ffn_backward(self.gate.hdr, self.gate.buf, self.up.hdr, self.up.buf, X, G, U, dH,
+                                     self.act, need_dx, need_dv, ws=ws, stream=stream)

@@ -1,10 +1,12 @@
 // api.cu -- status strings, version, header checks, the device status word.
+#include <cudaTypedefs.h>
 #include <string.h>
 
 #include <atomic>
 #include <mutex>
 
 #include "spw_internal.cuh"
+#include "spw_tcgen05.cuh"
 
 namespace {
 
@@ -16,6 +18,7 @@ std::atomic<long long> g_wait_limit{0};  // 0: the default, spw::kWaitLimitCycle
 std::atomic<int> g_column_fetch{0};
 int* g_status_ptr[spw::kMaxDevices];
 int g_sm_count[spw::kMaxDevices];
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::mutex g_mutex;
 
 }  // namespace
@@ -54,6 +57,32 @@ int column_fetch_mode() { return g_column_fetch.load(std::memory_order_relaxed);
 long long wait_limit_cycles() {
     const long long v = g_wait_limit.load(std::memory_order_relaxed);
     return v > 0 ? v : kWaitLimitCycles;
+}
+
+int encode_map_f16(CUtensorMap* map, const void* p, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
+                   uint32_t box_cols, uint32_t box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode;
+    {
+        std::lock_guard<std::mutex> lock(g_mutex);
+        if (!g_encode) {
+            void* fn = nullptr;
+            cudaDriverEntryPointQueryResult q;
+            if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q) !=
+                    cudaSuccess ||
+                q != cudaDriverEntryPointSuccess || !fn)
+                return SPW_ERR_CUDA;
+            g_encode = (PFN_cuTensorMapEncodeTiled_v12000)fn;
+        }
+        encode = g_encode;
+    }
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)ld_bytes};
+    const cuuint32_t box[2] = {box_cols, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult cr = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (void*)p, dims, strides, box, estr,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return cr == CUDA_SUCCESS ? SPW_OK : SPW_ERR_CUDA;
 }
 
 int check_header(const spw_format* h) {

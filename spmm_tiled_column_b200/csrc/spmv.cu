@@ -43,6 +43,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include "spw_act.cuh"
 #include "spw_internal.cuh"
 
 namespace spw {
@@ -117,6 +118,11 @@ struct SpmvParams {
     uint32_t* ffn_bits;   // ceil(N / 32) words
     uint32_t* ffn_pairs;  // per strip: finished layers (0, 1 or 2; left at 0)
     float ffn_t;
+    // Epilogue (spw_spmv_ep, one layer): y = act(sum + bias) + residual.
+    const uint16_t* bias;
+    const uint16_t* residual;
+    int ldr, act;
+    int ep;  // nonzero: apply it
 };
 
 __host__ __device__ constexpr int xt_stride(int B) {
@@ -480,6 +486,20 @@ __device__ void ffn_strip(const SpmvParams& p, int s, int lane) {
     }
 }
 
+// The result for row r of batch row b: the sum, or the epilogue on it (rows below N only;
+// kept out of line, so that the decode loop's registers do not pay for it).
+__device__ __noinline__ float epilogue_value(const SpmvParams& p, int b, int r, float v) {
+    if (p.bias) v += __half2float(__ushort_as_half(p.bias[r]));
+    v = act_f32(v, p.act);
+    if (p.residual) v += __half2float(__ushort_as_half(p.residual[(size_t)b * p.ldr + r]));
+    return v;
+}
+__device__ inline void store_result(const SpmvParams& p, const SpmvLayer& L, int b, int r, float v) {
+    if (r >= L.N) return;
+    if (p.ep) v = epilogue_value(p, b, r, v);
+    L.y[(size_t)b * L.ldy + r] = __half_as_ushort(__float2half_rn(v));
+}
+
 // End of tile i of a warp's range: when it closes the warp's piece of strip cur.s (the
 // strip's last k-tile, or the warp's last tile), write the piece's rows directly (a
 // strip held by one warp) or publish the fp32 partials and let the strip's last
@@ -501,9 +521,8 @@ __device__ inline void finish_piece(const SpmvParams& p, const SpmvLayer& L, con
     if (count == 1) {
 #pragma unroll
         for (int b = 0; b < B; b++) {
-            if (r0 < L.N) L.y[(size_t)b * L.ldy + r0] = __half_as_ushort(__float2half_rn(acc0[b]));
-            if (r0 + 1 < L.N)
-                L.y[(size_t)b * L.ldy + r0 + 1] = __half_as_ushort(__float2half_rn(acc1[b]));
+            store_result(p, L, b, r0, acc0[b]);
+            store_result(p, L, b, r0 + 1, acc1[b]);
         }
         finished = true;
     } else {
@@ -548,12 +567,11 @@ __device__ inline void finish_piece(const SpmvParams& p, const SpmvLayer& L, con
                 acc.z += __shfl_xor_sync(0xffffffffu, acc.z, 16);
                 acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
                 const int r = s * kStripRows + r4;
-                uint16_t* yb = L.y + (size_t)b * L.ldy;
                 if (half == 0) {
-                    if (r < L.N) yb[r] = __half_as_ushort(__float2half_rn(acc.x));
-                    if (r + 1 < L.N) yb[r + 1] = __half_as_ushort(__float2half_rn(acc.y));
-                    if (r + 2 < L.N) yb[r + 2] = __half_as_ushort(__float2half_rn(acc.z));
-                    if (r + 3 < L.N) yb[r + 3] = __half_as_ushort(__float2half_rn(acc.w));
+                    store_result(p, L, b, r, acc.x);
+                    store_result(p, L, b, r + 1, acc.y);
+                    store_result(p, L, b, r + 2, acc.z);
+                    store_result(p, L, b, r + 3, acc.w);
                 }
             }
             if (lane == 0) L.counters[s] = 0u;
@@ -1104,7 +1122,7 @@ int decode_group_launch(int n, const spw_format* hdrs, const void* const* bufs,
                         const uint16_t* const* xs, const int* ldxs,
                         const uint32_t* const* act_bits, uint16_t* const* ys, const int* ldys,
                         int B, float threshold, void* d_ws, uint64_t ws_bytes, cudaStream_t s,
-                        const FfnOut* ffn = nullptr) {
+                        const FfnOut* ffn = nullptr, const spw_epilogue* ep = nullptr) {
     if (n < 1 || n > kMaxGroup || !hdrs || !bufs || !xs || !ldxs || !ys || !ldys)
         return SPW_ERR_INVALID_ARG;
     if (!d_ws) return SPW_ERR_INVALID_ARG;
@@ -1173,6 +1191,13 @@ int decode_group_launch(int n, const spw_format* hdrs, const void* const* bufs,
         prm.ffn_bits = ffn->bits;
         prm.ffn_pairs = ffn->pairs;
         prm.ffn_t = ffn->t;
+    }
+    if (ep && (ep->bias || ep->residual || ep->act != SPW_ACT_NONE)) {
+        prm.bias = ep->bias;
+        prm.residual = ep->residual;
+        prm.ldr = ep->ldr;
+        prm.act = ep->act;
+        prm.ep = 1;
     }
     switch (B) {
 #define SPW_CASE(b) \
@@ -1280,6 +1305,18 @@ int spw_spmv(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, int 
     if (!hdr) return SPW_ERR_INVALID_ARG;
     return decode_group_launch(1, hdr, &d_buf, &d_x, &ldx, &d_act_bits, &d_y, &ldy, B, threshold,
                                d_ws, ws_bytes, (cudaStream_t)stream);
+}
+
+int spw_spmv_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, int B, int ldx,
+                float threshold, const uint32_t* d_act_bits, const spw_epilogue* ep, uint16_t* d_y,
+                int ldy, void* d_ws, uint64_t ws_bytes, void* stream) {
+    if (!hdr) return SPW_ERR_INVALID_ARG;
+    const int rc = check_header(hdr);
+    if (rc != SPW_OK) return rc;
+    const int erc = check_epilogue(ep, (int)hdr->N);
+    if (erc != SPW_OK) return erc;
+    return decode_group_launch(1, hdr, &d_buf, &d_x, &ldx, &d_act_bits, &d_y, &ldy, B, threshold,
+                               d_ws, ws_bytes, (cudaStream_t)stream, nullptr, ep);
 }
 
 int spw_spmv_group(int n, const spw_format* hdrs, const void* const* d_bufs,

@@ -272,6 +272,9 @@ int device_sm_count();
 int check_decode_args(const spw_format* hdr, const void* buf, const uint16_t* x, int B, int ldx,
                       float threshold, const uint32_t* act_bits, const uint16_t* y, int ldy);
 
+// Checks of an epilogue's arguments (null: no epilogue) for a result of N columns.
+int check_epilogue(const spw_epilogue* ep, int N);
+
 // Process-wide switch set by spw_set_launch_overlap.
 bool launch_overlap();
 
