@@ -19,8 +19,10 @@
 // p, p + pairs, ...; a unit is an output tile, or one of `parts` pieces of its reduction when
 // there are too few tiles; pieces go to fp32 partials in the workspace and the last CTA of a
 // tile to arrive adds them in order (deterministic) and runs the epilogue.
-//   warp 0, lane 0: TMA loads of this CTA's operand halves, `stages` deep.
-//   warp 1: rank 0 issues the MMAs of the pair; rank 1 relays "my stage has landed".
+//   warp 0, lane 0: TMA loads of this CTA's operand halves, `stages` deep; both CTAs' loads
+//     of a stage count on one barrier of rank 0 (a relay through rank 1, with an arrive at
+//     cluster scope for each stage, cost 0.3 us a step).
+//   warp 1: rank 0 issues the MMAs of the pair and commits each stage back to both CTAs.
 //   warps 2..9: epilogue; warp w reads the TMEM lanes 32 (w % 4).., one half of the columns.
 // Every wait is bounded and polls the pair's abort flags, as in spmm.cu.
 #include <string.h>
@@ -144,9 +146,9 @@ constexpr int kSmemLimit = 227 * 1024;
 struct GemmParams {
     int m_tiles, n_tiles, group_m, problem_tiles;
     int n_units, n_whole, parts;
-    int ksteps, kseg;  // reduction steps of a tile; those of its first segment (kDx)
+    int ksteps, kseg;  // reduction blocks of 64 of a tile; those of its first segment (kDx)
     int BN, stages;
-    uint32_t stage_bytes, off_bar;
+    uint32_t block_bytes, stage_bytes, off_bar;  // this CTA's operands, 64 deep; two of them
     int rows, cols;    // of the result (kFfn: of H)
     long long wait_limit;
     int* status;
@@ -200,6 +202,22 @@ __device__ inline Unit unit_of(const GemmParams& p, int u) {
     return w;
 }
 
+// Blocks of 64 along the reduction that the stage starting at block k holds: two, or one at
+// the end of the unit's range or (kDx) of a segment.  A stage of two halves the barrier
+// traffic for each MMA: 64-deep stages ran 0.39 us a block of 64 against 0.32.
+template <int MODE>
+__device__ inline int blocks_at(const GemmParams& p, int k, int k1) {
+    return k + 1 < k1 && (MODE != kDx || k + 1 != p.kseg) ? 2 : 1;
+}
+
+// The same barrier in both CTAs of the pair, once the MMAs issued so far have completed.
+__device__ inline void umma_commit_pair_multicast(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
 // MN-major operand, 128-byte swizzle: blocks of 64 (M or N) x 64 (K), each K row 128 bytes;
 // 8-row groups along K 1024 bytes apart, the 64-wide blocks 8192 bytes apart.
 __device__ inline uint64_t umma_desc_mn_sw128(uint32_t saddr) {
@@ -210,6 +228,20 @@ __device__ inline uint64_t umma_desc_mn_sw128(uint32_t saddr) {
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
     return d;
+}
+
+// This CTA's load, counted on a barrier of the pair that may be the other CTA's (no multicast).
+__device__ inline void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int c0, int c1, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"((uint64_t)map), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+// Counts bytes on a barrier without a copy.
+__device__ inline void mbar_complete_tx(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 // Joins the epilogue warps (named barrier 1) and tells whether all of them hold `ok`.
@@ -280,21 +312,20 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
     const int pair = (int)(blockIdx.x >> 1), pairs = (int)(gridDim.x >> 1);
     const int S = p.stages;
 
-    uint64_t* full = (uint64_t*)(smem + p.off_bar);
+    uint64_t* full = (uint64_t*)(smem + p.off_bar);  // on rank 0: both CTAs' loads of a stage
     uint64_t* empty = full + kMaxStages;
-    uint64_t* peer_ready = empty + kMaxStages;  // on rank 0: the other CTA's stage has landed
-    uint64_t* acc_full = peer_ready + kMaxStages;
+    uint64_t* acc_full = empty + kMaxStages;
     uint64_t* acc_empty = acc_full + 2;         // on rank 0: both CTAs' epilogue warps
     uint64_t* drain = acc_empty + 2;
     uint32_t* tmem_slot = (uint32_t*)(drain + 1);
     volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
     volatile uint32_t* last_flag = (volatile uint32_t*)(tmem_slot + 2);
+    volatile uint32_t* peer_issued = (volatile uint32_t*)(tmem_slot + 3);  // see the drain
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < S; i++) {
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), 1);
-            mbar_init(smem_u32(&peer_ready[i]), 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(smem_u32(&acc_full[i]), 1);
@@ -322,9 +353,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
     };
     const int half_cols = p.BN / 2;
 
-    long long issued = 0;  // producer: stages armed
+    uint32_t issued = 0;  // producer: stages loaded
     if (warp == 0) {
         if (lane == 0) {
+            const uint32_t full0 = map_to_rank(smem_u32(&full[0]), 0u);
             int s = 0;
             uint32_t ph = 0;
             bool ok = true;
@@ -332,29 +364,35 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                 const Unit w = unit_of(p, u);
                 const int arow = w.mt * 2 * kCtaRows + kCtaRows * (int)rank;
                 const int brow = MODE == kFfn ? w.nt * half_cols : w.nt * p.BN + half_cols * (int)rank;
-                for (int k = w.k0; k < w.k1; k++) {
+                for (int k = w.k0, n; k < w.k1; k += n) {
+                    n = blocks_at<MODE>(p, k, w.k1);
                     if (issued >= S && !wait_or_abort(smem_u32(&empty[s]), ph ^ 1u, abort_flag, p.wait_limit)) {
                         abort_both();
                         ok = false;
                         break;
                     }
-                    const uint32_t bar = smem_u32(&full[s]);
-                    const uint32_t a = sbase + (uint32_t)s * p.stage_bytes, b = a + kABytes;
-                    mbar_arrive_expect_tx(bar, p.stage_bytes);
+                    const uint32_t bar = full0 + 8u * (uint32_t)s;
+                    // the other CTA's bytes may land before this; the phase waits for the arrival
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2u * (uint32_t)n * p.block_bytes);
                     const bool second = MODE == kDx ? k >= p.kseg : w.prob != 0;
-                    const int kc = kBK * (MODE == kDx && second ? k - p.kseg : k);
                     const CUtensorMap* ma = second ? &ta1 : &ta0;
-                    if constexpr (A_MN) {
-                        tma_load_2d(a, ma, arow, kc, bar);
-                        tma_load_2d(a + 8192u, ma, arow + 64, kc, bar);
-                    } else {
-                        tma_load_2d(a, ma, kc, arow, bar);
-                    }
                     const CUtensorMap* mb = (MODE == kFfn ? rank != 0 : MODE == kDx && second) ? &tb1 : &tb0;
-                    if constexpr (B_MN) {
-                        for (int j = 0; j < half_cols / 64; j++) tma_load_2d(b + 8192u * j, mb, brow + 64 * j, kc, bar);
-                    } else {
-                        tma_load_2d(b, mb, kc, brow, bar);
+                    for (int i = 0; i < n; i++) {
+                        const uint32_t a = sbase + (uint32_t)s * p.stage_bytes + (uint32_t)i * p.block_bytes;
+                        const uint32_t b = a + kABytes;
+                        const int kc = kBK * (MODE == kDx && second ? k + i - p.kseg : k + i);
+                        if constexpr (A_MN) {
+                            tma_load_2d_pair(a, ma, arow, kc, bar);
+                            tma_load_2d_pair(a + 8192u, ma, arow + 64, kc, bar);
+                        } else {
+                            tma_load_2d_pair(a, ma, kc, arow, bar);
+                        }
+                        if constexpr (B_MN) {
+                            for (int j = 0; j < half_cols / 64; j++)
+                                tma_load_2d_pair(b + 8192u * j, mb, brow + 64 * j, kc, bar);
+                        } else {
+                            tma_load_2d_pair(b, mb, kc, brow, bar);
+                        }
                     }
                     issued++;
                     if (++s == S) { s = 0; ph ^= 1u; }
@@ -377,51 +415,35 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                     break;
                 }
                 tc_fence_after();
-                for (int k = w.k0; k < w.k1; k++) {
-                    if (!wait_or_abort(smem_u32(&full[s]), ph, abort_flag, p.wait_limit) ||
-                        !wait_or_abort_cluster(smem_u32(&peer_ready[s]), ph, abort_flag, p.wait_limit)) {
-                        abort_both();
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t sa = sbase + (uint32_t)s * p.stage_bytes, sb = sa + kABytes;
-#pragma unroll
-                    for (int j = 0; j < kBK / 16; j++) {
-                        const uint64_t ad = A_MN ? umma_desc_mn_sw128(sa + 2048u * j) : umma_desc_sw128(sa + 32u * j);
-                        const uint64_t bd = B_MN ? umma_desc_mn_sw128(sb + 2048u * j) : umma_desc_sw128(sb + 32u * j);
-                        umma_f16_pair(tmem + (uint32_t)(kAccCols * a), ad, bd, idesc, (k > w.k0 || j > 0) ? 1u : 0u);
-                    }
-                    umma_commit_pair_both(smem_u32(&empty[s]));
-                    if (++s == S) { s = 0; ph ^= 1u; }
-                }
-                if (ok) umma_commit_pair_both(smem_u32(&acc_full[a]));
-            }
-            umma_commit_pair_local(smem_u32(drain));
-            (void)mbar_drain(smem_u32(drain), 0);  // every issued MMA has completed
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        if (lane == 0) {  // rank 1: tell rank 0 that this CTA's stage has landed
-            const uint32_t ready0 = map_to_rank(smem_u32(&peer_ready[0]), 0u);
-            int s = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int u = pair; u < p.n_units && ok; u += pairs) {
-                const Unit w = unit_of(p, u);
-                for (int k = w.k0; k < w.k1; k++) {
+                for (int k = w.k0, n; k < w.k1; k += n) {
+                    n = blocks_at<MODE>(p, k, w.k1);
                     if (!wait_or_abort(smem_u32(&full[s]), ph, abort_flag, p.wait_limit)) {
                         abort_both();
                         ok = false;
                         break;
                     }
-                    mbar_arrive_cluster(ready0 + 8u * (uint32_t)s);
+                    tc_fence_after();
+                    for (int i = 0; i < n; i++) {
+                        const uint32_t sa = sbase + (uint32_t)s * p.stage_bytes + (uint32_t)i * p.block_bytes;
+                        const uint32_t sb = sa + kABytes;
+#pragma unroll
+                        for (int j = 0; j < kBK / 16; j++) {
+                            const uint64_t ad = A_MN ? umma_desc_mn_sw128(sa + 2048u * j) : umma_desc_sw128(sa + 32u * j);
+                            const uint64_t bd = B_MN ? umma_desc_mn_sw128(sb + 2048u * j) : umma_desc_sw128(sb + 32u * j);
+                            umma_f16_pair(tmem + (uint32_t)(kAccCols * a), ad, bd, idesc,
+                                          (k > w.k0 || i > 0 || j > 0) ? 1u : 0u);
+                        }
+                    }
+                    umma_commit_pair_multicast(smem_u32(&empty[s]));
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
+                if (ok) umma_commit_pair_multicast(smem_u32(&acc_full[a]));
             }
+            umma_commit_pair_local(smem_u32(drain));
+            (void)mbar_drain(smem_u32(drain), 0);  // every issued MMA has completed
         }
         __syncwarp();
-    } else {
+    } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue
         const int quarter = warp & 3, side = (warp - 2) >> 2;
         const int row = 32 * quarter + lane;  // accumulator row of this CTA
@@ -573,16 +595,36 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
 
     tc_fence_before();
     __syncthreads();
-    if (warp == 0 && lane == 0 && *abort_flag) {
-        // drain the copies this CTA armed: for each stage the phase of its last issue
-        for (int i = 0; i < S && i < issued; i++) {
-            const long long last = i + ((issued - 1 - i) / S) * S;
-            (void)mbar_drain(smem_u32(&full[i]), (uint32_t)((last / S) & 1));
-        }
-    }
+    // Rank 0's MMAs read both CTAs' shared memory, and each CTA arrives on the other's
+    // barriers: neither leaves before both are here, with their copies landed.  On an abort the
+    // producers may have stopped at different stages; rank 0, which owns the barriers, makes
+    // up for the difference and waits for every stage that either has loaded.
+    if (warp == 0 && lane == 0)
+        asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(map_to_rank(smem_u32((const void*)&peer_issued[rank]), 0u)),
+                     "r"(issued)
+                     : "memory");
     __syncthreads();
-    // rank 0's MMAs read both CTAs' shared memory, and each CTA arrives on the other's
-    // barriers: neither leaves before both are here
+    cluster_sync_all();
+    if (rank == 0 && warp == 0 && lane == 0 && *abort_flag) {
+        const uint32_t mine = peer_issued[0], theirs = peer_issued[1];
+        // (a stage's bytes follow from its place in the sequence of units)
+        const uint32_t most = mine > theirs ? mine : theirs;
+        uint32_t i = 0;
+        for (int u = pair; u < p.n_units && i < most; u += pairs) {
+            const Unit w = unit_of(p, u);
+            for (int k = w.k0, n; k < w.k1 && i < most; k += n, i++) {
+                n = blocks_at<MODE>(p, k, w.k1);
+                if (i >= theirs)  // armed for both, loaded by this CTA alone
+                    mbar_complete_tx(smem_u32(&full[i % S]), (uint32_t)n * p.block_bytes);
+                else if (i >= mine)  // loaded by the other alone
+                    mbar_arrive_expect_tx(smem_u32(&full[i % S]), (uint32_t)n * p.block_bytes);
+            }
+        }
+        for (i = most > (uint32_t)S ? most - S : 0u; i < most; i++)
+            (void)mbar_drain(smem_u32(&full[i % S]), (i / S) & 1u);
+    }
+    __syncwarp();
+    __syncthreads();
     cluster_sync_all();
     if (warp == 1) {
         tc_fence_after();
@@ -679,7 +721,7 @@ int gemm_pairs() {
 struct GemmPlan {
     int m_tiles, n_tiles, problems, BN, parts, n_whole, stages;
     long long tiles, n_units;
-    uint32_t stage_bytes, off_bar;
+    uint32_t block_bytes, stage_bytes, off_bar;
     size_t smem;
     uint64_t counter_bytes, partial_bytes;
 };
@@ -716,8 +758,9 @@ int plan_gemm(long long rows, long long cols, int problems, long long ksteps, in
     g->n_units = g->n_whole + split * g->parts;
     g->counter_bytes = round_up_u64(8ull * (uint64_t)split, 256);
     g->partial_bytes = 4ull * (uint64_t)split * g->parts * 2 * g->BN * kCtaRows;
-    g->stage_bytes = kABytes + (uint32_t)g->BN / 2 * 128;
-    const uint32_t bars = 8u * (3 * kMaxStages + 5) + 16u;
+    g->block_bytes = kABytes + (uint32_t)g->BN / 2 * 128;
+    g->stage_bytes = 2 * g->block_bytes;
+    const uint32_t bars = 8u * (2 * kMaxStages + 5) + 32u;
     g->stages = (int)((kSmemLimit - 1024 - bars) / g->stage_bytes);
     if (g->stages > kMaxStages) g->stages = kMaxStages;
     g->off_bar = (uint32_t)g->stages * g->stage_bytes;
@@ -737,6 +780,7 @@ void fill_params(const GemmPlan& g, long long ksteps, GemmParams* p) {
     p->ksteps = p->kseg = (int)ksteps;
     p->BN = g.BN;
     p->stages = g.stages;
+    p->block_bytes = g.block_bytes;
     p->stage_bytes = g.stage_bytes;
     p->off_bar = g.off_bar;
     p->wait_limit = wait_limit_cycles();
