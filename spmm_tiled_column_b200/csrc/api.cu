@@ -60,7 +60,7 @@ long long wait_limit_cycles() {
 }
 
 int encode_map_f16(CUtensorMap* map, const void* p, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
-                   uint32_t box_cols, uint32_t box_rows) {
+                   uint32_t box_cols, uint32_t box_rows, bool swizzle) {
     PFN_cuTensorMapEncodeTiled_v12000 encode;
     {
         std::lock_guard<std::mutex> lock(g_mutex);
@@ -80,7 +80,8 @@ int encode_map_f16(CUtensorMap* map, const void* p, uint64_t cols, uint64_t rows
     const cuuint32_t box[2] = {box_cols, box_rows};
     const cuuint32_t estr[2] = {1, 1};
     const CUresult cr = encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, (void*)p, dims, strides, box, estr,
-                               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                               CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return cr == CUDA_SUCCESS ? SPW_OK : SPW_ERR_CUDA;
 }

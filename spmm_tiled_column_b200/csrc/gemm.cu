@@ -58,6 +58,7 @@ struct ExpandLayer {
 struct ExpandParams {
     ExpandLayer L[2];
     long long tiles;    // both layers
+    int strips, ktp;    // strips of an output block; blocks of a row of blocks
     uint32_t warp_smem;
     int* status;
 };
@@ -103,18 +104,17 @@ __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const __grid_
         __syncwarp();
         const long long strip = t / L.n_ktiles;
         const int kt = (int)(t - strip * L.n_ktiles);
-        const size_t ld = (size_t)L.n_ktiles * kTileCols;
-        const int g = lane & 7, rp = 2 * (lane >> 3);
-        uint16_t* out = L.out + ((size_t)strip * kStripRows + rp) * ld + (size_t)kt * kTileCols + 8 * g;
+        const int q = 2 * (lane & 15);
+        const uint2* rc = rec + (lane < 16 ? 0 : kRecPerHalf);
+        unsigned char* out = (unsigned char*)L.out + ((strip / p.strips) * p.ktp + kt) * (size_t)(p.strips * 8192) +
+                             (strip % p.strips) * 1024 + 32 * lane;
 #pragma unroll
-        for (int it = 0; it < 8; it++) {
+        for (int g = 0; g < 8; g++) {
             uint32_t o0[4] = {0u, 0u, 0u, 0u}, o1[4] = {0u, 0u, 0u, 0u};
             if (ok) {
-                const uint2* rc = rec + (it >= 4 ? kRecPerHalf : 0) + 9 * g;
-                const int q = 8 * (it & 3) + rp;
 #pragma unroll
                 for (int c = 0; c < 8; c++) {
-                    const uint2 e = rc[c];
+                    const uint2 e = rc[9 * g + c];
                     const uint32_t hi = e.x >> q >> 1;
                     const uint32_t a = e.y - 2u * (uint32_t)__popc(hi);
                     // both loads stay inside the tile's values, or in the slack before them
@@ -124,8 +124,9 @@ __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const __grid_
                     o1[c >> 1] |= (hi & 1u ? v1 : 0u) << sft;
                 }
             }
-            *(uint4*)(out + (size_t)(8 * it) * ld) = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-            *(uint4*)(out + (size_t)(8 * it + 1) * ld) = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+            uint4* o = (uint4*)(out + (size_t)g * (p.strips * 1024));
+            o[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
+            o[1] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
         }
         __syncwarp();
     }
@@ -168,6 +169,7 @@ struct GemmParams {
     uint64_t values_units[2];
     uint16_t* dv[2];
     int n_strips, n_ktiles;
+    int ktp;             // expanded weight: blocks in a row of blocks
 };
 
 struct Unit {
@@ -227,6 +229,18 @@ __device__ inline uint64_t umma_desc_mn_sw128(uint32_t saddr) {
     d |= (uint64_t)(1024 >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// No swizzle: core matrices of 8 rows x 16 bytes, 128 contiguous bytes each; lbo and sbo are
+// the strides between them along K and along M or N (K-major), or the other way round
+// (MN-major: a core matrix is then 8 K rows of 8 M or N elements).
+__device__ inline uint64_t umma_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(sbo >> 4) << 32;
+    d |= (uint64_t)1 << 46;
     return d;
 }
 
@@ -378,8 +392,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                     const CUtensorMap* ma = second ? &ta1 : &ta0;
                     const CUtensorMap* mb = (MODE == kFfn ? rank != 0 : MODE == kDx && second) ? &tb1 : &tb0;
                     for (int i = 0; i < n; i++) {
-                        const uint32_t a = sbase + (uint32_t)s * p.stage_bytes + (uint32_t)i * p.block_bytes;
-                        const uint32_t b = a + kABytes;
+                        const uint32_t a = sbase + (uint32_t)s * p.stage_bytes + (uint32_t)i * kABytes;
+                        const uint32_t b = sbase + (uint32_t)s * p.stage_bytes + 2 * kABytes + (uint32_t)(i * half_cols * 128);
                         const int kc = kBK * (MODE == kDx && second ? k + i - p.kseg : k + i);
                         if constexpr (A_MN) {
                             tma_load_2d_pair(a, ma, arow, kc, bar);
@@ -387,11 +401,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                         } else {
                             tma_load_2d_pair(a, ma, kc, arow, bar);
                         }
-                        if constexpr (B_MN) {
+                        if constexpr (MODE == kDv) {
                             for (int j = 0; j < half_cols / 64; j++)
                                 tma_load_2d_pair(b + 8192u * j, mb, brow + 64 * j, kc, bar);
+                        } else if constexpr (MODE == kDx) {
+                            tma_load_2d_pair(b, mb, 0, 64 * (kc / kBK * p.ktp) + brow, bar);
                         } else {
-                            tma_load_2d_pair(b, mb, kc, brow, bar);
+                            tma_load_2d_pair(b, mb, 0, (brow / half_cols * p.ktp + k + i) * half_cols, bar);
                         }
                     }
                     issued++;
@@ -424,12 +440,14 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                     }
                     tc_fence_after();
                     for (int i = 0; i < n; i++) {
-                        const uint32_t sa = sbase + (uint32_t)s * p.stage_bytes + (uint32_t)i * p.block_bytes;
-                        const uint32_t sb = sa + kABytes;
+                        const uint32_t sa = sbase + (uint32_t)s * p.stage_bytes + (uint32_t)i * kABytes;
+                        const uint32_t sb = sbase + (uint32_t)s * p.stage_bytes + 2 * kABytes + (uint32_t)(i * half_cols * 128);
 #pragma unroll
                         for (int j = 0; j < kBK / 16; j++) {
                             const uint64_t ad = A_MN ? umma_desc_mn_sw128(sa + 2048u * j) : umma_desc_sw128(sa + 32u * j);
-                            const uint64_t bd = B_MN ? umma_desc_mn_sw128(sb + 2048u * j) : umma_desc_sw128(sb + 32u * j);
+                            const uint64_t bd = MODE == kDv   ? umma_desc_mn_sw128(sb + 2048u * j)
+                                                : MODE == kDx ? umma_desc_plain(sb + 256u * j, 128, 1024)
+                                                              : umma_desc_plain(sb + 32u * j * half_cols, 16u * half_cols, 128);
                             umma_f16_pair(tmem + (uint32_t)(kAccCols * a), ad, bd, idesc,
                                           (k > w.k0 || i > 0 || j > 0) ? 1u : 0u);
                         }
@@ -807,14 +825,18 @@ int launch_gemm(const GemmPlan& g, const CUtensorMap& a0, const CUtensorMap& a1,
     return SPW_OK;
 }
 
+int ktp_of(const spw_format* h) { return (int)round_up_u64(h->n_ktiles, 4); }
+
 uint64_t dense_bytes(const spw_format* h) {
-    return 2ull * h->n_strips * kStripRows * h->n_ktiles * kTileCols;
+    return round_up_u64(h->n_strips, 4) * (uint64_t)ktp_of(h) * 8192;
 }
 
 // Expands one or two weights (dense row stride 64 n_ktiles).
-int expand(int n, const spw_format* const* hdrs, const void* const* bufs, uint16_t* const* outs, cudaStream_t s) {
+int expand(int n, const spw_format* const* hdrs, const void* const* bufs, uint16_t* const* outs, int strips, cudaStream_t s) {
     ExpandParams p;
     memset(&p, 0, sizeof(p));
+    p.strips = strips;
+    p.ktp = ktp_of(hdrs[0]);
     uint32_t units = 0;
     for (int l = 0; l < n; l++) {
         const spw_format& h = *hdrs[l];
@@ -913,9 +935,8 @@ int run_dx(const spw_format* h, int weights, const Layout& L, uint8_t* ws, uint3
     for (int w = 0; w < weights; w++) {
         int rc = encode_map_f16(&a[w], dY[w], h->N, (uint64_t)M, ld_bytes[w], kBK, kCtaRows);
         if (rc != SPW_OK) return rc;
-        const uint64_t kcols = (uint64_t)h->n_ktiles * kTileCols;
-        rc = encode_map_f16(&b[w], ws + L.dense + w * dense_bytes(h), kcols, (uint64_t)h->n_strips * kStripRows,
-                            2 * kcols, 64, kBK);
+        rc = encode_map_f16(&b[w], ws + L.dense + w * dense_bytes(h), 64, dense_bytes(h) / 128, 128, 64,
+                            (uint32_t)g.BN / 2, false);
         if (rc != SPW_OK) return rc;
     }
     if (weights == 1) {
@@ -926,6 +947,7 @@ int run_dx(const spw_format* h, int weights, const Layout& L, uint8_t* ws, uint3
     fill_params(g, (long long)weights * h->n_strips, &p);
     if (!p.status) return SPW_ERR_CUDA;
     p.kseg = (int)h->n_strips;
+    p.ktp = ktp_of(h);
     p.rows = M;
     p.cols = (int)h->K;
     p.Y = dX;
@@ -1007,15 +1029,14 @@ int spw_spmm_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_X, i
     uint8_t* ws = (uint8_t*)d_ws;
     cudaStream_t s = (cudaStream_t)stream;
     CUtensorMap a, b;
-    const uint64_t kcols = (uint64_t)hdr->n_ktiles * kTileCols;
     rc = encode_map_f16(&a, d_X, hdr->K, (uint64_t)M, map_ld(ldx, M), kBK, kCtaRows);
     if (rc == SPW_OK)
-        rc = encode_map_f16(&b, ws + L.dense, kcols, (uint64_t)hdr->n_strips * kStripRows, 2 * kcols, kBK,
-                            (uint32_t)L.fwd.BN / 2);
+        rc = encode_map_f16(&b, ws + L.dense, 64, dense_bytes(hdr) / 128, 128, 64, (uint32_t)L.fwd.BN / 2, false);
     if (rc != SPW_OK) return rc;
     GemmParams p;
     fill_params(L.fwd, hdr->n_ktiles, &p);
     if (!p.status) return SPW_ERR_CUDA;
+    p.ktp = ktp_of(hdr);
     p.rows = M;
     p.cols = N;
     p.Y = d_Y;
@@ -1031,7 +1052,7 @@ int spw_spmm_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_X, i
     p.partials = (float*)(ws + L.partials);
     if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
     uint16_t* dense[1] = {(uint16_t*)(ws + L.dense)};
-    rc = expand(1, &hdr, &d_buf, dense, s);
+    rc = expand(1, &hdr, &d_buf, dense, L.fwd.BN / 128, s);
     if (rc != SPW_OK) return rc;
     return launch_gemm<kEp>(L.fwd, a, a, b, b, p, gemm_pairs(), s);
 }
@@ -1071,15 +1092,14 @@ int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_f
     cudaStream_t s = (cudaStream_t)stream;
     uint16_t* dense[2] = {(uint16_t*)(ws + L.dense), (uint16_t*)(ws + L.dense + dense_bytes(hdr_gate))};
     CUtensorMap a, b[2];
-    const uint64_t kcols = (uint64_t)hdr_gate->n_ktiles * kTileCols;
     rc = encode_map_f16(&a, d_X, (uint64_t)K, (uint64_t)M, map_ld(ldx, M), kBK, kCtaRows);
     for (int w = 0; w < 2 && rc == SPW_OK; w++)
-        rc = encode_map_f16(&b[w], dense[w], kcols, (uint64_t)hdr_gate->n_strips * kStripRows, 2 * kcols, kBK,
-                            (uint32_t)L.fwd.BN / 2);
+        rc = encode_map_f16(&b[w], dense[w], 64, dense_bytes(hdr_gate) / 128, 128, 64, (uint32_t)L.fwd.BN / 2, false);
     if (rc != SPW_OK) return rc;
     GemmParams p;
     fill_params(L.fwd, hdr_gate->n_ktiles, &p);
     if (!p.status) return SPW_ERR_CUDA;
+    p.ktp = ktp_of(hdr_gate);
     p.rows = M;
     p.cols = N;
     p.Y = d_H;
@@ -1095,7 +1115,7 @@ int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_f
     if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
     const spw_format* hdrs[2] = {hdr_gate, hdr_up};
     const void* bufs[2] = {d_buf_gate, d_buf_up};
-    rc = expand(2, hdrs, bufs, dense, s);
+    rc = expand(2, hdrs, bufs, dense, L.fwd.BN / 128, s);
     if (rc != SPW_OK) return rc;
     return launch_gemm<kFfn>(L.fwd, a, a, b[0], b[1], p, gemm_pairs(), s);
 }
@@ -1154,7 +1174,7 @@ int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate, co
     uint32_t* counters = (uint32_t*)ws;
     if (d_dX) {
         uint16_t* dense[2] = {(uint16_t*)(ws + L.dense), (uint16_t*)(ws + L.dense + dense_bytes(hdr_gate))};
-        rc = expand(2, hdrs, bufs, dense, s);
+        rc = expand(2, hdrs, bufs, dense, 1, s);
         if (rc == SPW_OK) rc = run_dx(hdr_gate, 2, L, ws, counters, dY, ld_bytes, M, d_dX, lddx, s);
         if (rc != SPW_OK) return rc;
     }
@@ -1198,7 +1218,7 @@ int spw_spmm_backward(const spw_format* hdr, const void* d_buf, const uint16_t* 
     if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
     if (d_dX) {
         uint16_t* dense[1] = {(uint16_t*)(ws + L.dense)};
-        rc = expand(1, &hdr, &d_buf, dense, s);
+        rc = expand(1, &hdr, &d_buf, dense, 1, s);
         if (rc == SPW_OK) rc = run_dx(hdr, 1, L, ws, counters, &d_dY, ld_bytes, M, d_dX, lddx, s);
         if (rc != SPW_OK) return rc;
     }

@@ -10,9 +10,9 @@
 namespace spw {
 
 // Tensor map of a row-major fp16 matrix (rows x cols at ld_bytes, a multiple of 16) for
-// boxes of box_rows x box_cols with the 128-byte swizzle; elements outside it read as 0.
+// boxes of box_rows x box_cols, with the 128-byte swizzle or none; elements outside it read as 0.
 int encode_map_f16(CUtensorMap* map, const void* p, uint64_t cols, uint64_t rows, uint64_t ld_bytes,
-                   uint32_t box_cols, uint32_t box_rows);
+                   uint32_t box_cols, uint32_t box_rows, bool swizzle = true);
 
 // ------------------------------------------------------------------ tcgen05 helpers
 __device__ inline uint64_t umma_desc_sw128(uint32_t saddr) {
