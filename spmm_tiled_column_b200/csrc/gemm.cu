@@ -29,20 +29,25 @@
 
 #include <mutex>
 
-#include "spw_act.cuh"
-#include "spw_internal.cuh"
+#include "spw_prefill.cuh"
 #include "spw_tcgen05.cuh"
 
 namespace spw {
 namespace {
 
 // ------------------------------------------------------------------ expansion
+// 32 bytes to a 32-byte aligned address.
+__device__ inline void st_global_32b(void* at, const uint32_t (&a)[4], const uint32_t (&b)[4]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at), "r"(a[0]), "r"(a[1]), "r"(a[2]),
+                 "r"(a[3]), "r"(b[0]), "r"(b[1]), "r"(b[2]), "r"(b[3])
+                 : "memory");
+}
+
 constexpr int kExpandWarps = 8;
-// A warp's 64 columns x 2 halves of records {bits, end of the half's values}; one record of
-// padding after every 8 columns puts the 8 column groups a warp reads together in
-// different banks.
-constexpr int kRecPerHalf = 72;
-constexpr uint32_t kRecBytes = 2 * kRecPerHalf * 8;
+// A warp's records {bits, end of the half's values} of 64 columns: low halves, high halves (16
+// bytes off, in other banks).
+constexpr uint32_t kRecHalf = 64 * 8 + 16;
+constexpr uint32_t kRecBytes = 2 * kRecHalf;
 
 struct ExpandLayer {
     const uint64_t* bitmaps;
@@ -63,16 +68,18 @@ struct ExpandParams {
     int* status;
 };
 
-// One warp writes one 64 x 64 tile of the dense weight (row stride 64 n_ktiles).  Lane
-// (row pair r, column group c) = (lane / 8, lane % 8) writes 16-byte chunks, so a store of
-// the warp covers whole 128-byte lines of 4 rows.  Row pair (2r, 2r+1) of a column: the kept
-// rows from 2r+1 upward within its half are the last popc(bits >> (2r+1)) values of that
-// half, so row 2r+1's value ends there and row 2r's stands just before it.
+// One warp writes one 64 x 64 tile of the dense weight, in the blocks that the product reads: p.strips
+// strips by one k-tile, [8 columns][row][8 columns of it], 16 bytes a row.  Lane l has the rows 2l and
+// 2l+1, so a store of the warp covers 1024 bytes.  Bound by memory: the compressed weight in, 2 bytes an
+// entry out (4096 x 8192 at 50 %: 105 MB in 20 us, 5.2 TB/s).
 __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const __grid_constant__ ExpandParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned char* mine = smem + (size_t)warp * p.warp_smem;
-    uint2* rec = (uint2*)mine;
+    unsigned char* rec = mine;
+    const int up = 30 - 2 * (lane & 15);
+    const uint32_t above = 0xFFFFFFFEu << (2 * (lane & 15));
+    const uint4* recp = (const uint4*)(rec + (lane < 16 ? 0u : kRecHalf));
     unsigned char* vals = mine + kRecBytes;  // 16 bytes of slack first: see the loads below
     const uint32_t vals_s = smem_u32(vals) + 16u;
     for (long long i = (long long)blockIdx.x * kExpandWarps + warp; i < p.tiles;
@@ -95,17 +102,12 @@ __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const __grid_
             const uint4* src = (const uint4*)(L.values + (size_t)u0 * 8);
             for (uint32_t j = lane; j < u1 - u0; j += 32) ((uint4*)(vals + 16))[j] = __ldg(src + j);
             const uint32_t a0 = vals_s + 2u * (uint32_t)(incl - c0 - c1), a1 = a0 + 2u * (uint32_t)c0;
-            const int r = 2 * lane + (2 * lane >> 3);  // 2l and 2l+1 lie in one group of 8
-            rec[r] = make_uint2(bw.x, a0 + 2u * (uint32_t)cl0);
-            rec[r + 1] = make_uint2(bw.z, a1 + 2u * (uint32_t)cl1);
-            rec[kRecPerHalf + r] = make_uint2(bw.y, a1);
-            rec[kRecPerHalf + r + 1] = make_uint2(bw.w, a1 + 2u * (uint32_t)c1);
+            *(uint4*)(rec + 16 * lane) = make_uint4(bw.x, a0 + 2u * (uint32_t)cl0, bw.z, a1 + 2u * (uint32_t)cl1);
+            *(uint4*)(rec + kRecHalf + 16 * lane) = make_uint4(bw.y, a1, bw.w, a1 + 2u * (uint32_t)c1);
         }
         __syncwarp();
         const long long strip = t / L.n_ktiles;
         const int kt = (int)(t - strip * L.n_ktiles);
-        const int q = 2 * (lane & 15);
-        const uint2* rc = rec + (lane < 16 ? 0 : kRecPerHalf);
         unsigned char* out = (unsigned char*)L.out + ((strip / p.strips) * p.ktp + kt) * (size_t)(p.strips * 8192) +
                              (strip % p.strips) * 1024 + 32 * lane;
 #pragma unroll
@@ -113,28 +115,15 @@ __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const __grid_
             uint32_t o0[4] = {0u, 0u, 0u, 0u}, o1[4] = {0u, 0u, 0u, 0u};
             if (ok) {
 #pragma unroll
-                for (int c = 0; c < 8; c++) {
-                    const uint2 e = rc[9 * g + c];
-                    const uint32_t hi = e.x >> q >> 1;
-                    const uint32_t a = e.y - 2u * (uint32_t)__popc(hi);
-                    // both loads stay inside the tile's values, or in the slack before them
-                    const uint32_t v1 = lds_u16(a), v0 = lds_u16(a - 2u);
-                    const uint32_t sft = 16u * (c & 1);
-                    o0[c >> 1] |= ((e.x >> q) & 1u ? v0 : 0u) << sft;
-                    o1[c >> 1] |= (hi & 1u ? v1 : 0u) << sft;
-                }
+                for (int c = 0; c < 4; c++) decode_pair(recp[4 * g + c], above, up, o0[c], o1[c]);
             }
-            uint4* o = (uint4*)(out + (size_t)g * (p.strips * 1024));
-            o[0] = make_uint4(o0[0], o0[1], o0[2], o0[3]);
-            o[1] = make_uint4(o1[0], o1[1], o1[2], o1[3]);
+            st_global_32b(out + (size_t)g * (p.strips * 1024), o0, o1);
         }
         __syncwarp();
     }
 }
 
 // ------------------------------------------------------------------ the product
-enum Mode { kEp, kFfn, kDx, kDv };
-
 constexpr int kCtaRows = 128;  // accumulator rows per CTA; 256 per pair
 constexpr int kBK = 64;
 constexpr int kEpiWarps = 8;
@@ -150,19 +139,11 @@ struct GemmParams {
     int ksteps, kseg;  // reduction blocks of 64 of a tile; those of its first segment (kDx)
     int BN, stages;
     uint32_t block_bytes, stage_bytes, off_bar;  // this CTA's operands, 64 deep; two of them
-    int rows, cols;    // of the result (kFfn: of H)
     long long wait_limit;
     int* status;
     uint32_t* counters;  // arrivals per split tile and rank
     float* partials;     // [split tile][part][rank][BN][128]
-    // results and what the epilogue reads
-    uint16_t* Y;
-    const uint16_t* bias;
-    const uint16_t* residual;
-    uint16_t* G;
-    uint16_t* U;
-    int ldy, ldr, ldg, ldu, act;
-    int vec;             // bit 0: Y, 1: residual, 2: G, 3: U take 16-byte accesses
+    PrefillOut o;
     // kDv: per weight, its pattern and the packed gradient
     const uint64_t* bitmaps[2];
     const uint32_t* tileptr[2];
@@ -483,7 +464,8 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                 // CTA's rows) goes on with the sum of all, the others are done.
                 float* tile_part = p.partials + (((size_t)w.stile * p.parts) * 2 + rank) * (size_t)p.BN * kCtaRows;
                 float* out = tile_part + (size_t)w.part * 2 * p.BN * kCtaRows;
-                for (int c = side * half_cols; c < (side + 1) * half_cols; c += 32) {
+                const bool rows_in = w.mt * 2 * kCtaRows + kCtaRows * (int)rank + 32 * quarter < p.o.rows;
+                for (int c = side * half_cols; c < (side + 1) * half_cols && rows_in; c += 32) {
                     uint32_t r[32];
                     tmem_ld32(acc + (uint32_t)c, r);
 #pragma unroll
@@ -523,38 +505,39 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                 }
             };
             const int r = w.mt * 2 * kCtaRows + kCtaRows * (int)rank + row;  // result row
+            const bool rows_in = r - lane < p.o.rows;                        // some row of the warp's
             if constexpr (MODE == kEp || MODE == kDx) {
-                for (int c = side * half_cols; c < (side + 1) * half_cols; c += 32) {
+                for (int c = side * half_cols; c < (side + 1) * half_cols && rows_in; c += 32) {
                     float v[32];
                     load(c, v);
                     const int col = w.nt * p.BN + c;
-                    if (r >= p.rows || col >= p.cols) continue;
+                    if (r >= p.o.rows || col >= p.o.cols) continue;
                     if constexpr (MODE == kEp) {
-                        if (p.bias) add32(p.bias, col, p.cols, true, v);
-                        if (p.act != SPW_ACT_NONE) {
+                        if (p.o.bias) add32(p.o.bias, col, p.o.cols, true, v);
+                        if (p.o.act != SPW_ACT_NONE) {
 #pragma unroll
-                            for (int j = 0; j < 32; j++) v[j] = act_f32(v[j], p.act);
+                            for (int j = 0; j < 32; j++) v[j] = act_f32(v[j], p.o.act);
                         }
-                        if (p.residual) add32(p.residual + (size_t)r * p.ldr, col, p.cols, p.vec & 2, v);
+                        if (p.o.residual) add32(p.o.residual + (size_t)r * p.o.ldr, col, p.o.cols, p.o.vec & 2, v);
                     }
-                    store32(p.Y + (size_t)r * p.ldy, col, p.cols, p.vec & 1, v);
+                    store32(p.o.Y + (size_t)r * p.o.ldy, col, p.o.cols, p.o.vec & 1, v);
                 }
             } else if constexpr (MODE == kFfn) {
                 // columns 0 .. BN/2-1 hold the gate, the others the up product of the same
                 // BN/2 result columns
-                for (int c = side * (half_cols / 2); c < (side + 1) * (half_cols / 2); c += 32) {
+                for (int c = side * (half_cols / 2); c < (side + 1) * (half_cols / 2) && rows_in; c += 32) {
                     float g[32], v[32];
                     load(c, g);
                     load(half_cols + c, v);
                     const int col = w.nt * half_cols + c;
-                    if (r >= p.rows || col >= p.cols) continue;
-                    if (p.G) {
-                        store32(p.G + (size_t)r * p.ldg, col, p.cols, p.vec & 4, g);
-                        store32(p.U + (size_t)r * p.ldu, col, p.cols, p.vec & 8, v);
+                    if (r >= p.o.rows || col >= p.o.cols) continue;
+                    if (p.o.G) {
+                        store32(p.o.G + (size_t)r * p.o.ldg, col, p.o.cols, p.o.vec & 4, g);
+                        store32(p.o.U + (size_t)r * p.o.ldu, col, p.o.cols, p.o.vec & 8, v);
                     }
 #pragma unroll
-                    for (int j = 0; j < 32; j++) v[j] *= act_f32(g[j], p.act);
-                    store32(p.Y + (size_t)r * p.ldy, col, p.cols, p.vec & 1, v);
+                    for (int j = 0; j < 32; j++) v[j] *= act_f32(g[j], p.o.act);
+                    store32(p.o.Y + (size_t)r * p.o.ldy, col, p.o.cols, p.o.vec & 1, v);
                 }
             } else {
                 // Packed gradient: row r of the weight is bit r % 64 of its strip's words; a
@@ -562,7 +545,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                 // before k and of the column's rows above it.
                 const int strip = r / kStripRows;  // two quarters, one strip: warp-uniform
                 const int hi = quarter & 1;        // this warp's half of the strip's rows
-                for (int c = side * half_cols; c < (side + 1) * half_cols; c += 64) {
+                for (int c = side * half_cols; c < (side + 1) * half_cols && rows_in; c += 64) {
                     float v[32];
                     const int kt = (w.nt * p.BN + c) / kTileCols;
                     const bool in = strip < p.n_strips && kt < p.n_ktiles;  // warp-uniform
@@ -742,6 +725,7 @@ struct GemmPlan {
     uint32_t block_bytes, stage_bytes, off_bar;
     size_t smem;
     uint64_t counter_bytes, partial_bytes;
+    double cost;  // microseconds
 };
 
 // Column tile and split of the reduction from a small cost model in microseconds: a step of
@@ -771,6 +755,7 @@ int plan_gemm(long long rows, long long cols, int problems, long long ksteps, in
         }
     }
     if (g->tiles * g->parts > 0x3fffffffll) return SPW_ERR_UNSUPPORTED;
+    g->cost = best;
     g->n_whole = g->parts > 1 ? 0 : (int)g->tiles;
     const long long split = g->tiles - g->n_whole;
     g->n_units = g->n_whole + split * g->parts;
@@ -879,30 +864,52 @@ bool vec_ok(const void* p, int ld) { return !p || (ld % 8 == 0 && aligned16(p));
 // where there are any, and the fp32 partials (shared by the products, which run in turn).
 struct Layout {
     GemmPlan fwd, dx, dv;
-    uint64_t counters, dense, grads, partials, total;
+    bool fwd_direct, dx_direct;  // by the direct form (spmm_direct.cu): no workspace
+    uint64_t dv_counters, counters, dense, grads, partials, total;  // counters: the bytes to clear
     int ldn;
 };
 
 constexpr int kForward = 1, kDxOut = 2, kDvOut = 4;
 
-int make_layout(const spw_format* h, int weights, int M, int what, bool gated_forward, Layout* L) {
+// Whether the direct form takes less time than expansion and product.  Expansion reads the
+// compressed weight and writes 2 bytes an entry: about 3.1 bytes an entry at 5.2 TB/s, after
+// 4 us, and the clearing of counters another 2.
+bool choose_direct(int mode, const spw_format* h, const spw_format* h2, int M, const GemmPlan& g) {
+    const double entries = (h2 ? 2.0 : 1.0) * h->n_strips * (double)h->n_ktiles * kStripRows * kTileCols;
+    const double other = g.cost + 4.0 + entries * 3.1 / 5.2e6 + (g.counter_bytes ? 2.0 : 0.0);
+    const double direct = direct_cost(mode, h, h2, M);
+    return direct >= 0.0 && direct <= other;
+}
+
+// h2: the second weight's header, or null.
+int make_layout(const spw_format* h, const spw_format* h2, int M, int what, Layout* L) {
     const int pairs = gemm_pairs();
+    const int weights = h2 ? 2 : 1;
     memset(L, 0, sizeof(*L));
     L->ldn = (int)round_up_u64(h->N, 8);
-    uint64_t c = 0, part = 0;
+    uint64_t c = 0, part = 0, dense = 0;
     int rc;
     if (what & kForward) {
-        rc = plan_gemm(M, gated_forward ? 2ll * h->N : (long long)h->N, 1, h->n_ktiles, pairs, &L->fwd);
+        rc = plan_gemm(M, (long long)weights * h->N, 1, h->n_ktiles, pairs, &L->fwd);
         if (rc != SPW_OK) return rc;
-        c = L->fwd.counter_bytes;
-        part = L->fwd.partial_bytes;
+        L->fwd_direct = choose_direct(h2 ? kFfn : kEp, h, h2, M, L->fwd);
+        if (!L->fwd_direct) {
+            c = L->fwd.counter_bytes;
+            part = L->fwd.partial_bytes;
+            dense = (uint64_t)weights * dense_bytes(h);
+        }
     }
     if (what & kDxOut) {
         rc = plan_gemm(M, h->K, 1, (long long)weights * h->n_strips, pairs, &L->dx);
         if (rc != SPW_OK) return rc;
-        c += L->dx.counter_bytes;
-        if (L->dx.partial_bytes > part) part = L->dx.partial_bytes;
+        L->dx_direct = choose_direct(kDx, h, h2, M, L->dx);
+        if (!L->dx_direct) {
+            c += L->dx.counter_bytes;
+            if (L->dx.partial_bytes > part) part = L->dx.partial_bytes;
+            dense = (uint64_t)weights * dense_bytes(h);
+        }
     }
+    L->dv_counters = c;
     if (what & kDvOut) {
         rc = plan_gemm(h->N, h->K, weights, ((long long)M + 63) / 64, pairs, &L->dv);
         if (rc != SPW_OK) return rc;
@@ -911,7 +918,6 @@ int make_layout(const spw_format* h, int weights, int M, int what, bool gated_fo
     }
     L->counters = c;
     L->dense = c;
-    const uint64_t dense = what & (kForward | kDxOut) ? (uint64_t)weights * dense_bytes(h) : 0;
     L->grads = L->dense + dense;
     const uint64_t grads =
         weights == 2 && (what & (kDxOut | kDvOut)) ? 2 * round_up_u64(2ull * (uint64_t)M * L->ldn, 256) : 0;
@@ -921,16 +927,86 @@ int make_layout(const spw_format* h, int weights, int M, int what, bool gated_fo
 }
 
 int check_ws(const void* d_ws, uint64_t ws_bytes, const Layout& L) {
+    if (!L.total) return SPW_OK;
     if (!d_ws) return SPW_ERR_INVALID_ARG;
     if (ws_bytes < L.total) return SPW_ERR_BUFFER_TOO_SMALL;
     if (!aligned16(d_ws)) return SPW_ERR_ALIGNMENT;
     return SPW_OK;
 }
 
-// dX = sum over the weights of dY_w W_w, from the expanded weights.
-int run_dx(const spw_format* h, int weights, const Layout& L, uint8_t* ws, uint32_t* counters, const uint16_t* const* dY,
-           const uint64_t* ld_bytes, int M, uint16_t* dX, int lddx, cudaStream_t s) {
+// A forward product (kEp: one weight; kFfn: gate and up) by the form that the layout chose.
+template <int MODE>
+int run_forward(const Layout& L, const spw_format* const* hdrs, const void* const* bufs, const uint16_t* X, int M, int ldx,
+                const PrefillOut& o, uint8_t* ws, cudaStream_t s) {
+    constexpr int kWeights = MODE == kFfn ? 2 : 1;
+    const spw_format* h = hdrs[0];
+    if (L.fwd_direct) {
+        DirectCall c;
+        memset(&c, 0, sizeof(c));
+        c.mode = MODE;
+        for (int w = 0; w < kWeights; w++) {
+            c.h[w] = hdrs[w];
+            c.buf[w] = bufs[w];
+        }
+        c.x[0] = X;
+        c.ldx_bytes[0] = map_ld(ldx, M);
+        c.M = M;
+        c.out = o;
+        return direct_launch(c, s);
+    }
+    const GemmPlan& g = L.fwd;
+    CUtensorMap a, b[2];
+    uint16_t* dense[2];
+    int rc = encode_map_f16(&a, X, h->K, (uint64_t)M, map_ld(ldx, M), kBK, kCtaRows);
+    for (int w = 0; w < kWeights && rc == SPW_OK; w++) {
+        dense[w] = (uint16_t*)(ws + L.dense + (uint64_t)w * dense_bytes(h));
+        rc = encode_map_f16(&b[w], dense[w], 64, dense_bytes(h) / 128, 128, 64, (uint32_t)g.BN / 2, false);
+    }
+    if (rc != SPW_OK) return rc;
+    GemmParams p;
+    fill_params(g, h->n_ktiles, &p);
+    if (!p.status) return SPW_ERR_CUDA;
+    p.o = o;
+    p.ktp = ktp_of(h);
+    p.counters = (uint32_t*)ws;
+    p.partials = (float*)(ws + L.partials);
+    if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
+    rc = expand(kWeights, hdrs, bufs, dense, g.BN / 128, s);
+    if (rc != SPW_OK) return rc;
+    return launch_gemm<MODE>(g, a, a, b[0], b[kWeights - 1], p, gemm_pairs(), s);
+}
+
+// dX = sum over the weights of dY_w W_w, by the form that the layout chose.
+int run_dx(const spw_format* const* hdrs, const void* const* bufs, int weights, const Layout& L, uint8_t* ws,
+           uint32_t* counters, const uint16_t* const* dY, const uint64_t* ld_bytes, int M, uint16_t* dX, int lddx,
+           cudaStream_t s) {
     const GemmPlan& g = L.dx;
+    const spw_format* h = hdrs[0];
+    PrefillOut o;
+    memset(&o, 0, sizeof(o));
+    o.rows = M;
+    o.cols = (int)h->K;
+    o.Y = dX;
+    o.ldy = lddx;
+    o.vec = vec_ok(dX, lddx) ? 1 : 0;
+    if (L.dx_direct) {
+        DirectCall c;
+        memset(&c, 0, sizeof(c));
+        c.mode = kDx;
+        for (int w = 0; w < weights; w++) {
+            c.h[w] = hdrs[w];
+            c.buf[w] = bufs[w];
+            c.x[w] = dY[w];
+            c.ldx_bytes[w] = ld_bytes[w];
+        }
+        c.M = M;
+        c.out = o;
+        return direct_launch(c, s);
+    }
+    uint16_t* dense[2];
+    for (int w = 0; w < weights; w++) dense[w] = (uint16_t*)(ws + L.dense + (uint64_t)w * dense_bytes(h));
+    const int erc = expand(weights, hdrs, bufs, dense, 1, s);
+    if (erc != SPW_OK) return erc;
     CUtensorMap a[2], b[2];
     for (int w = 0; w < weights; w++) {
         int rc = encode_map_f16(&a[w], dY[w], h->N, (uint64_t)M, ld_bytes[w], kBK, kCtaRows);
@@ -948,11 +1024,7 @@ int run_dx(const spw_format* h, int weights, const Layout& L, uint8_t* ws, uint3
     if (!p.status) return SPW_ERR_CUDA;
     p.kseg = (int)h->n_strips;
     p.ktp = ktp_of(h);
-    p.rows = M;
-    p.cols = (int)h->K;
-    p.Y = dX;
-    p.ldy = lddx;
-    p.vec = vec_ok(dX, lddx) ? 1 : 0;
+    p.o = o;
     p.counters = counters;
     p.partials = (float*)(ws + L.partials);
     return launch_gemm<kDx>(g, a[0], a[1], b[0], b[1], p, gemm_pairs(), s);
@@ -982,8 +1054,8 @@ int run_dv(const spw_format* const* hdrs, const void* const* bufs, int weights, 
     if (weights == 1) a[1] = a[0];
     p.n_strips = (int)h->n_strips;
     p.n_ktiles = (int)h->n_ktiles;
-    p.rows = (int)h->N;
-    p.cols = (int)h->K;
+    p.o.rows = (int)h->N;
+    p.o.cols = (int)h->K;
     p.counters = counters;
     p.partials = (float*)(ws + L.partials);
     return launch_gemm<kDv>(g, a[0], a[1], b, b, p, gemm_pairs(), s);
@@ -1007,7 +1079,7 @@ extern "C" {
 
 uint64_t spw_spmm_ep_workspace_bytes(const spw_format* hdr, int M) {
     Layout L;
-    if (check_header(hdr) != SPW_OK || M < 1 || make_layout(hdr, 1, M, kForward, false, &L) != SPW_OK) return 0;
+    if (check_header(hdr) != SPW_OK || M < 1 || make_layout(hdr, nullptr, M, kForward, &L) != SPW_OK) return 0;
     return L.total;
 }
 
@@ -1023,38 +1095,24 @@ int spw_spmm_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_X, i
     if (!ld_ok(ldx, (int)hdr->K, M) || ldy < N) return SPW_ERR_INVALID_ARG;
     if (!aligned16(d_buf) || !aligned16(d_X) || !aligned16(d_Y)) return SPW_ERR_ALIGNMENT;
     Layout L;
-    rc = make_layout(hdr, 1, M, kForward, false, &L);
+    rc = make_layout(hdr, nullptr, M, kForward, &L);
     if (rc == SPW_OK) rc = check_ws(d_ws, ws_bytes, L);
     if (rc != SPW_OK) return rc;
-    uint8_t* ws = (uint8_t*)d_ws;
     cudaStream_t s = (cudaStream_t)stream;
-    CUtensorMap a, b;
-    rc = encode_map_f16(&a, d_X, hdr->K, (uint64_t)M, map_ld(ldx, M), kBK, kCtaRows);
-    if (rc == SPW_OK)
-        rc = encode_map_f16(&b, ws + L.dense, 64, dense_bytes(hdr) / 128, 128, 64, (uint32_t)L.fwd.BN / 2, false);
-    if (rc != SPW_OK) return rc;
-    GemmParams p;
-    fill_params(L.fwd, hdr->n_ktiles, &p);
-    if (!p.status) return SPW_ERR_CUDA;
-    p.ktp = ktp_of(hdr);
-    p.rows = M;
-    p.cols = N;
-    p.Y = d_Y;
-    p.ldy = ldy;
+    PrefillOut o;
+    memset(&o, 0, sizeof(o));
+    o.rows = M;
+    o.cols = N;
+    o.Y = d_Y;
+    o.ldy = ldy;
     if (ep) {
-        p.bias = ep->bias;
-        p.act = ep->act;
-        p.residual = ep->residual;
-        p.ldr = ep->ldr;
+        o.bias = ep->bias;
+        o.act = ep->act;
+        o.residual = ep->residual;
+        o.ldr = ep->ldr;
     }
-    p.vec = (vec_ok(d_Y, ldy) ? 1 : 0) | (vec_ok(p.residual, p.ldr) ? 2 : 0);
-    p.counters = (uint32_t*)ws;
-    p.partials = (float*)(ws + L.partials);
-    if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
-    uint16_t* dense[1] = {(uint16_t*)(ws + L.dense)};
-    rc = expand(1, &hdr, &d_buf, dense, L.fwd.BN / 128, s);
-    if (rc != SPW_OK) return rc;
-    return launch_gemm<kEp>(L.fwd, a, a, b, b, p, gemm_pairs(), s);
+    o.vec = (vec_ok(d_Y, ldy) ? 1 : 0) | (vec_ok(o.residual, o.ldr) ? 2 : 0);
+    return run_forward<kEp>(L, &hdr, &d_buf, d_X, M, ldx, o, (uint8_t*)d_ws, s);
 }
 
 static int check_ffn_pair(const spw_format* hg, const spw_format* hu) {
@@ -1066,7 +1124,7 @@ static int check_ffn_pair(const spw_format* hg, const spw_format* hu) {
 
 uint64_t spw_spmm_ffn_workspace_bytes(const spw_format* hdr_gate, const spw_format* hdr_up, int M) {
     Layout L;
-    if (check_ffn_pair(hdr_gate, hdr_up) != SPW_OK || M < 1 || make_layout(hdr_gate, 2, M, kForward, true, &L) != SPW_OK)
+    if (check_ffn_pair(hdr_gate, hdr_up) != SPW_OK || M < 1 || make_layout(hdr_gate, hdr_up, M, kForward, &L) != SPW_OK)
         return 0;
     return L.total;
 }
@@ -1085,45 +1143,31 @@ int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_f
         !aligned16(d_U))
         return SPW_ERR_ALIGNMENT;
     Layout L;
-    rc = make_layout(hdr_gate, 2, M, kForward, true, &L);
+    rc = make_layout(hdr_gate, hdr_up, M, kForward, &L);
     if (rc == SPW_OK) rc = check_ws(d_ws, ws_bytes, L);
     if (rc != SPW_OK) return rc;
-    uint8_t* ws = (uint8_t*)d_ws;
     cudaStream_t s = (cudaStream_t)stream;
-    uint16_t* dense[2] = {(uint16_t*)(ws + L.dense), (uint16_t*)(ws + L.dense + dense_bytes(hdr_gate))};
-    CUtensorMap a, b[2];
-    rc = encode_map_f16(&a, d_X, (uint64_t)K, (uint64_t)M, map_ld(ldx, M), kBK, kCtaRows);
-    for (int w = 0; w < 2 && rc == SPW_OK; w++)
-        rc = encode_map_f16(&b[w], dense[w], 64, dense_bytes(hdr_gate) / 128, 128, 64, (uint32_t)L.fwd.BN / 2, false);
-    if (rc != SPW_OK) return rc;
-    GemmParams p;
-    fill_params(L.fwd, hdr_gate->n_ktiles, &p);
-    if (!p.status) return SPW_ERR_CUDA;
-    p.ktp = ktp_of(hdr_gate);
-    p.rows = M;
-    p.cols = N;
-    p.Y = d_H;
-    p.ldy = ldh;
-    p.G = d_G;
-    p.ldg = ldg;
-    p.U = d_U;
-    p.ldu = ldu;
-    p.act = act;
-    p.vec = (vec_ok(d_H, ldh) ? 1 : 0) | (vec_ok(d_G, ldg) ? 4 : 0) | (vec_ok(d_U, ldu) ? 8 : 0);
-    p.counters = (uint32_t*)ws;
-    p.partials = (float*)(ws + L.partials);
-    if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
+    PrefillOut o;
+    memset(&o, 0, sizeof(o));
+    o.rows = M;
+    o.cols = N;
+    o.Y = d_H;
+    o.ldy = ldh;
+    o.G = d_G;
+    o.ldg = ldg;
+    o.U = d_U;
+    o.ldu = ldu;
+    o.act = act;
+    o.vec = (vec_ok(d_H, ldh) ? 1 : 0) | (vec_ok(d_G, ldg) ? 4 : 0) | (vec_ok(d_U, ldu) ? 8 : 0);
     const spw_format* hdrs[2] = {hdr_gate, hdr_up};
     const void* bufs[2] = {d_buf_gate, d_buf_up};
-    rc = expand(2, hdrs, bufs, dense, L.fwd.BN / 128, s);
-    if (rc != SPW_OK) return rc;
-    return launch_gemm<kFfn>(L.fwd, a, a, b[0], b[1], p, gemm_pairs(), s);
+    return run_forward<kFfn>(L, hdrs, bufs, d_X, M, ldx, o, (uint8_t*)d_ws, s);
 }
 
 uint64_t spw_spmm_ffn_backward_workspace_bytes(const spw_format* hdr_gate, const spw_format* hdr_up, int M) {
     Layout L;
     if (check_ffn_pair(hdr_gate, hdr_up) != SPW_OK || M < 1 ||
-        make_layout(hdr_gate, 2, M, kDxOut | kDvOut, false, &L) != SPW_OK)
+        make_layout(hdr_gate, hdr_up, M, kDxOut | kDvOut, &L) != SPW_OK)
         return 0;
     return L.total;
 }
@@ -1153,7 +1197,7 @@ int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate, co
     if (ldg < N || ldu < N || lddh < N || (d_dX && lddx < K) || (d_dV_gate && !ld_ok(ldx, K, M)))
         return SPW_ERR_INVALID_ARG;
     Layout L;
-    rc = make_layout(hdr_gate, 2, M, kDxOut | kDvOut, false, &L);
+    rc = make_layout(hdr_gate, hdr_up, M, kDxOut | kDvOut, &L);
     if (rc == SPW_OK) rc = check_ws(d_ws, ws_bytes, L);
     if (rc != SPW_OK) return rc;
     uint8_t* ws = (uint8_t*)d_ws;
@@ -1173,21 +1217,19 @@ int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate, co
     const uint64_t ld_bytes[2] = {2ull * L.ldn, 2ull * L.ldn};
     uint32_t* counters = (uint32_t*)ws;
     if (d_dX) {
-        uint16_t* dense[2] = {(uint16_t*)(ws + L.dense), (uint16_t*)(ws + L.dense + dense_bytes(hdr_gate))};
-        rc = expand(2, hdrs, bufs, dense, 1, s);
-        if (rc == SPW_OK) rc = run_dx(hdr_gate, 2, L, ws, counters, dY, ld_bytes, M, d_dX, lddx, s);
+        rc = run_dx(hdrs, bufs, 2, L, ws, counters, dY, ld_bytes, M, d_dX, lddx, s);
         if (rc != SPW_OK) return rc;
     }
     if (d_dV_gate) {
         uint16_t* dV[2] = {d_dV_gate, d_dV_up};
-        rc = run_dv(hdrs, bufs, 2, L, ws, counters + L.dx.counter_bytes / 4, dY, ld_bytes, d_X, ldx, M, dV, s);
+        rc = run_dv(hdrs, bufs, 2, L, ws, counters + L.dv_counters / 4, dY, ld_bytes, d_X, ldx, M, dV, s);
     }
     return rc;
 }
 
 uint64_t spw_spmm_backward_workspace_bytes(const spw_format* hdr, int M) {
     Layout L;
-    if (check_header(hdr) != SPW_OK || M < 1 || make_layout(hdr, 1, M, kDxOut | kDvOut, false, &L) != SPW_OK) return 0;
+    if (check_header(hdr) != SPW_OK || M < 1 || make_layout(hdr, nullptr, M, kDxOut | kDvOut, &L) != SPW_OK) return 0;
     return L.total;
 }
 
@@ -1209,7 +1251,7 @@ int spw_spmm_backward(const spw_format* hdr, const void* d_buf, const uint16_t* 
     if (!d_buf || !d_dY || (d_dV && !d_X)) return SPW_ERR_INVALID_ARG;
     if (!ld_ok(lddy, N, M) || (d_dX && lddx < K) || (d_dV && !ld_ok(ldx, K, M))) return SPW_ERR_INVALID_ARG;
     Layout L;
-    rc = make_layout(hdr, 1, M, kDxOut | kDvOut, false, &L);
+    rc = make_layout(hdr, nullptr, M, kDxOut | kDvOut, &L);
     if (rc == SPW_OK) rc = check_ws(d_ws, ws_bytes, L);
     if (rc != SPW_OK) return rc;
     uint8_t* ws = (uint8_t*)d_ws;
@@ -1217,13 +1259,11 @@ int spw_spmm_backward(const spw_format* hdr, const void* d_buf, const uint16_t* 
     const uint64_t ld_bytes[1] = {map_ld(lddy, M)};
     if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
     if (d_dX) {
-        uint16_t* dense[1] = {(uint16_t*)(ws + L.dense)};
-        rc = expand(1, &hdr, &d_buf, dense, 1, s);
-        if (rc == SPW_OK) rc = run_dx(hdr, 1, L, ws, counters, &d_dY, ld_bytes, M, d_dX, lddx, s);
+        rc = run_dx(&hdr, &d_buf, 1, L, ws, counters, &d_dY, ld_bytes, M, d_dX, lddx, s);
         if (rc != SPW_OK) return rc;
     }
     if (d_dV)
-        rc = run_dv(&hdr, &d_buf, 1, L, ws, counters + L.dx.counter_bytes / 4, &d_dY, ld_bytes, d_X, ldx, M, &d_dV, s);
+        rc = run_dv(&hdr, &d_buf, 1, L, ws, counters + L.dv_counters / 4, &d_dY, ld_bytes, d_X, ldx, M, &d_dV, s);
     return rc;
 }
 
