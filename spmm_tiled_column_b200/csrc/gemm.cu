@@ -398,49 +398,57 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
         }
         __syncwarp();
     } else if (warp == 1 && rank == 0) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_f16(2 * kCtaRows, p.BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-            int s = 0, it = 0;
-            uint32_t ph = 0;
-            bool ok = true;
-            for (int u = pair; u < p.n_units && ok; u += pairs, it++) {
-                const Unit w = unit_of(p, u);
-                const int a = it & 1;
-                if (it >= 2 && !wait_or_abort_cluster(smem_u32(&acc_empty[a]), (uint32_t)(((it >> 1) & 1) ^ 1),
-                                                      abort_flag, p.wait_limit)) {
-                    abort_both();
+        // ------------------------------------------------------------ MMAs
+        const uint32_t idesc = idesc_f16(2 * kCtaRows, p.BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+        const uint32_t b0 = sbase + 2 * kABytes;
+        const uint64_t ad0 = A_MN ? umma_desc_mn_sw128(sbase) : umma_desc_sw128(sbase);
+        const uint64_t bd0 = MODE == kDv   ? umma_desc_mn_sw128(b0)
+                             : MODE == kDx ? umma_desc_plain(b0, 128, 1024)
+                                           : umma_desc_plain(b0, 16u * half_cols, 128);
+        // from a slice of 16 along the reduction to the next
+        const uint32_t da = A_MN ? 2048u : 32u, db = MODE == kDv ? 2048u : MODE == kDx ? 256u : 32u * half_cols;
+        int s = 0, it = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int u = pair; u < p.n_units && ok; u += pairs, it++) {
+            const Unit w = unit_of(p, u);
+            const int a = it & 1;
+            if (it >= 2) {
+                ok = __all_sync(0xffffffffu, wait_or_abort_cluster(smem_u32(&acc_empty[a]), (uint32_t)(((it >> 1) & 1) ^ 1),
+                                                                   abort_flag, p.wait_limit));
+                if (!ok) {
+                    if (lane == 0) abort_both();
+                    break;
+                }
+            }
+            tc_fence_after();
+            for (int k = w.k0, n; k < w.k1; k += n) {
+                n = blocks_at<MODE>(p, k, w.k1);
+                ok = __all_sync(0xffffffffu, wait_or_abort(smem_u32(&full[s]), ph, abort_flag, p.wait_limit));
+                if (!ok) {
+                    if (lane == 0) abort_both();
                     break;
                 }
                 tc_fence_after();
-                for (int k = w.k0, n; k < w.k1; k += n) {
-                    n = blocks_at<MODE>(p, k, w.k1);
-                    if (!wait_or_abort(smem_u32(&full[s]), ph, abort_flag, p.wait_limit)) {
-                        abort_both();
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t so = (uint32_t)s * p.stage_bytes;
                     for (int i = 0; i < n; i++) {
-                        const uint32_t sa = sbase + (uint32_t)s * p.stage_bytes + (uint32_t)i * kABytes;
-                        const uint32_t sb = sbase + (uint32_t)s * p.stage_bytes + 2 * kABytes + (uint32_t)(i * half_cols * 128);
 #pragma unroll
-                        for (int j = 0; j < kBK / 16; j++) {
-                            const uint64_t ad = A_MN ? umma_desc_mn_sw128(sa + 2048u * j) : umma_desc_sw128(sa + 32u * j);
-                            const uint64_t bd = MODE == kDv   ? umma_desc_mn_sw128(sb + 2048u * j)
-                                                : MODE == kDx ? umma_desc_plain(sb + 256u * j, 128, 1024)
-                                                              : umma_desc_plain(sb + 32u * j * half_cols, 16u * half_cols, 128);
-                            umma_f16_pair(tmem + (uint32_t)(kAccCols * a), ad, bd, idesc,
+                        for (int j = 0; j < kBK / 16; j++)
+                            umma_f16_pair(tmem + (uint32_t)(kAccCols * a), ad0 + ((so + (uint32_t)i * kABytes + da * j) >> 4),
+                                          bd0 + ((so + (uint32_t)(i * half_cols * 128) + db * j) >> 4), idesc,
                                           (k > w.k0 || i > 0 || j > 0) ? 1u : 0u);
-                        }
                     }
                     umma_commit_pair_multicast(smem_u32(&empty[s]));
-                    if (++s == S) { s = 0; ph ^= 1u; }
+                    if (k + n >= w.k1) umma_commit_pair_multicast(smem_u32(&acc_full[a]));
                 }
-                if (ok) umma_commit_pair_multicast(smem_u32(&acc_full[a]));
+                __syncwarp();
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
-            umma_commit_pair_local(smem_u32(drain));
-            (void)mbar_drain(smem_u32(drain), 0);  // every issued MMA has completed
         }
+        if (elect_one()) umma_commit_pair_local(smem_u32(drain));
+        __syncwarp();
+        (void)mbar_drain(smem_u32(drain), 0);  // every issued MMA has completed
         __syncwarp();
     } else if (warp >= 2) {
         // ------------------------------------------------------------ epilogue

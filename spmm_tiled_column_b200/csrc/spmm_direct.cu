@@ -226,21 +226,22 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {  // ------------------------------------------ MMAs
-            const uint32_t idesc = idesc_f16(128, tok) | (MODE == kDx ? 1u << 15 : 0u);
-            // the same operand bytes, 16 of the reduction a slice
-            constexpr uint32_t kSliceA = MODE == kDx ? 256u : 4096u;
-            const uint64_t ad0 = MODE == kDx ? desc_plain(sbase + p.off_w, 128, 1024) : desc_plain(sbase + p.off_w, 2048, 128);
-            const uint64_t bd0 = umma_desc_sw128(sbase);
-            uint32_t xo = 0, wo = 0;  // the slots' offsets
-            for (int n = 0; n < nk; n++) {
-                const uint32_t ph = (uint32_t)(n / kRing) & 1u;
-                if (!wait_or_abort(smem_u32(&x_full[n % kRing]), ph, abort_flag, p.wait_limit) ||
-                    !wait_or_abort(smem_u32(&w_full[n % kRing]), ph, abort_flag, p.wait_limit)) {
-                    flag_abort(abort_flag, p.status);
-                    break;
-                }
-                tc_fence_after();
+        // ---------------------------------------------------------- MMAs
+        const uint32_t idesc = idesc_f16(128, tok) | (MODE == kDx ? 1u << 15 : 0u);
+        // the same operand bytes, 16 of the reduction a slice
+        constexpr uint32_t kSliceA = MODE == kDx ? 256u : 4096u;
+        const uint64_t ad0 = MODE == kDx ? desc_plain(sbase + p.off_w, 128, 1024) : desc_plain(sbase + p.off_w, 2048, 128);
+        const uint64_t bd0 = umma_desc_sw128(sbase);
+        uint32_t xo = 0, wo = 0;  // the slots' offsets
+        for (int n = 0; n < nk; n++) {
+            const uint32_t ph = (uint32_t)(n / kRing) & 1u;
+            if (!__all_sync(0xffffffffu, wait_or_abort(smem_u32(&x_full[n % kRing]), ph, abort_flag, p.wait_limit) &&
+                                             wait_or_abort(smem_u32(&w_full[n % kRing]), ph, abort_flag, p.wait_limit))) {
+                if (lane == 0) flag_abort(abort_flag, p.status);
+                break;
+            }
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int j = 0; j < kBK / 16; j++) {
                     const uint64_t ad = ad0 + ((wo + kSliceA * j) >> 4), bd = bd0 + ((xo + 32u * j) >> 4);
@@ -251,13 +252,17 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
                 }
                 umma_commit(smem_u32(&x_empty[n % kRing]));
                 umma_commit(smem_u32(&w_empty[n % kRing]));
-                xo = xo + p.x_bytes == (uint32_t)p.sx * p.x_bytes ? 0u : xo + p.x_bytes;
-                wo = wo + kWBytes == (uint32_t)p.sw * kWBytes ? 0u : wo + kWBytes;
             }
+            __syncwarp();
+            xo = xo + p.x_bytes == (uint32_t)p.sx * p.x_bytes ? 0u : xo + p.x_bytes;
+            wo = wo + kWBytes == (uint32_t)p.sw * kWBytes ? 0u : wo + kWBytes;
+        }
+        if (elect_one()) {
             umma_commit(smem_u32(acc_full));
             umma_commit(smem_u32(drain));
-            (void)mbar_drain(smem_u32(drain), 0);
         }
+        __syncwarp();
+        (void)mbar_drain(smem_u32(drain), 0);
         __syncwarp();
     } else if (warp == 2) {
         // ---------------------------------------------------------- compressed tiles

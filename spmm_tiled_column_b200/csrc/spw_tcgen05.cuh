@@ -92,6 +92,19 @@ __device__ inline void tc_fence_before() {
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  Code that issues tcgen05 instructions runs with all
+// lanes and elects the issuer around them: the operands then stay in uniform registers (one
+// lane running the whole loop behind a lane test cost about 250 cycles an MMA).
+__device__ inline bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e)::"memory");
+    return e != 0;
+}
+
 // ---- SM-pair (cta_group::2) helpers: a cluster of two CTAs computes one 256-row tile;
 // CTA rank 0 issues the MMAs for both.
 __device__ inline uint32_t cluster_rank() {
