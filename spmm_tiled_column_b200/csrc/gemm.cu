@@ -139,6 +139,7 @@ struct GemmParams {
     int ksteps, kseg;  // reduction blocks of 64 of a tile; those of its first segment (kDx)
     int BN, stages;
     uint32_t block_bytes, stage_bytes, off_bar;  // this CTA's operands, 64 deep; two of them
+    uint32_t off_stage;  // the epilogue warps' blocks
     long long wait_limit;
     int* status;
     uint32_t* counters;  // arrivals per split tile and rank
@@ -258,25 +259,12 @@ __device__ inline uint32_t pack2(float a, float b) {
     return *(const uint32_t*)&h;
 }
 
-// 32 values of one row to columns col .. col+31 of a row-major fp16 matrix (cols wide).
-__device__ inline void store32(uint16_t* row, int col, int cols, bool vec, const float (&v)[32]) {
-    if (vec && col + 32 <= cols) {
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            *(uint4*)(row + col + 8 * j) = make_uint4(pack2(v[8 * j], v[8 * j + 1]), pack2(v[8 * j + 2], v[8 * j + 3]),
-                                                      pack2(v[8 * j + 4], v[8 * j + 5]), pack2(v[8 * j + 6], v[8 * j + 7]));
-    } else {
-#pragma unroll
-        for (int j = 0; j < 32; j++)
-            if (col + j < cols) row[col + j] = __half_as_ushort(__float2half_rn(v[j]));
-    }
-}
-
-__device__ inline void add32(const uint16_t* row, int col, int cols, bool vec, float (&v)[32]) {
-    if (vec && col + 32 <= cols) {
+// Adds 32 values of a bias to columns col .. col+31.
+__device__ inline void add_bias(const uint16_t* bias, int col, int cols, float (&v)[32]) {
+    if (col + 32 <= cols) {
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const uint4 r = *(const uint4*)(row + col + 8 * j);
+            const uint4 r = *(const uint4*)(bias + col + 8 * j);
             const uint32_t w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
             for (int e = 0; e < 4; e++) {
@@ -288,7 +276,78 @@ __device__ inline void add32(const uint16_t* row, int col, int cols, bool vec, f
     } else {
 #pragma unroll
         for (int j = 0; j < 32; j++)
-            if (col + j < cols) v[j] += __half2float(__ushort_as_half(row[col + j]));
+            if (col + j < cols) v[j] += __half2float(__ushort_as_half(bias[col + j]));
+    }
+}
+
+// Writes a warp's 32 x 32 block (lane l holds row l, columns col .. col+31) to rows row0 .. of
+// a row-major fp16 matrix, plus the residual's block if there is one.  Where 16-byte accesses
+// are allowed each lane writes its own row.  Elsewhere the block goes through the warp's piece
+// of shared memory (rows 33 floats apart: no two lanes in one bank), so that a row's 64 bytes
+// go out together: with a lane writing 2 bytes at a time of its own row, a ragged leading
+// dimension took longer than the whole product (500 x 1300, 4096 tokens: 34 us against 18; the
+// aligned 4096 x 1024 takes 47 us through shared memory, 40 us without).
+// pairs: even leading dimensions, so two columns a lane.
+__device__ inline void store_block(float* stage, int lane, uint16_t* Y, int ldy, const uint16_t* residual, int ldr, int row0,
+                                   int rows, int col, int cols, bool vec, bool pairs, const float (&v)[32]) {
+    if (vec && col + 32 <= cols) {
+        if (row0 + lane >= rows) return;
+        const size_t r = (size_t)(row0 + lane);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (residual) q = *(const uint4*)(residual + r * ldr + col + 8 * j);
+            const uint32_t in[4] = {q.x, q.y, q.z, q.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                float2 f = make_float2(v[8 * j + 2 * e], v[8 * j + 2 * e + 1]);
+                if (residual) {
+                    const float2 a = __half22float2(*(const __half2*)&in[e]);
+                    f.x += a.x;
+                    f.y += a.y;
+                }
+                o[e] = pack2(f.x, f.y);
+            }
+            *(uint4*)(Y + r * ldy + col + 8 * j) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+        return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 32; j++) stage[lane * 33 + j] = v[j];
+    __syncwarp();
+    const int n = min(32, rows - row0);
+    if (pairs) {
+        const int c = 2 * (lane & 15), hi = lane >> 4;
+        if (col + c + 1 < cols) {
+#pragma unroll 8
+            for (int i = hi; i < n; i += 2) {
+                const size_t r = (size_t)(row0 + i);
+                float2 f = make_float2(stage[i * 33 + c], stage[i * 33 + c + 1]);
+                if (residual) {
+                    const float2 q = __half22float2(*(const __half2*)(residual + r * ldr + col + c));
+                    f.x += q.x;
+                    f.y += q.y;
+                }
+                *(uint32_t*)(Y + r * ldy + col + c) = pack2(f.x, f.y);
+            }
+        } else if (col + c < cols) {
+            for (int i = hi; i < n; i += 2) {
+                const size_t r = (size_t)(row0 + i);
+                float f = stage[i * 33 + c];
+                if (residual) f += __half2float(__ushort_as_half(residual[r * ldr + col + c]));
+                Y[r * ldy + col + c] = __half_as_ushort(__float2half_rn(f));
+            }
+        }
+    } else if (col + lane < cols) {
+#pragma unroll 8
+        for (int i = 0; i < n; i++) {
+            const size_t r = (size_t)(row0 + i);
+            float f = stage[i * 33 + lane];
+            if (residual) f += __half2float(__ushort_as_half(residual[r * ldr + col + lane]));
+            Y[r * ldy + col + lane] = __half_as_ushort(__float2half_rn(f));
+        }
     }
 }
 
@@ -514,38 +573,40 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
             };
             const int r = w.mt * 2 * kCtaRows + kCtaRows * (int)rank + row;  // result row
             const bool rows_in = r - lane < p.o.rows;                        // some row of the warp's
+            const int r0 = r - lane;  // the warp's first row
+            float* stage = (float*)(smem + p.off_stage) + (warp - 2) * (32 * 33);
             if constexpr (MODE == kEp || MODE == kDx) {
                 for (int c = side * half_cols; c < (side + 1) * half_cols && rows_in; c += 32) {
+                    const int col = w.nt * p.BN + c;
+                    if (col >= p.o.cols) break;
                     float v[32];
                     load(c, v);
-                    const int col = w.nt * p.BN + c;
-                    if (r >= p.o.rows || col >= p.o.cols) continue;
                     if constexpr (MODE == kEp) {
-                        if (p.o.bias) add32(p.o.bias, col, p.o.cols, true, v);
+                        if (p.o.bias) add_bias(p.o.bias, col, p.o.cols, v);
                         if (p.o.act != SPW_ACT_NONE) {
 #pragma unroll
                             for (int j = 0; j < 32; j++) v[j] = act_f32(v[j], p.o.act);
                         }
-                        if (p.o.residual) add32(p.o.residual + (size_t)r * p.o.ldr, col, p.o.cols, p.o.vec & 2, v);
                     }
-                    store32(p.o.Y + (size_t)r * p.o.ldy, col, p.o.cols, p.o.vec & 1, v);
+                    store_block(stage, lane, p.o.Y, p.o.ldy, MODE == kEp ? p.o.residual : nullptr, p.o.ldr, r0, p.o.rows, col,
+                                p.o.cols, (p.o.vec & 3) == 3, p.o.vec & 16, v);
                 }
             } else if constexpr (MODE == kFfn) {
                 // columns 0 .. BN/2-1 hold the gate, the others the up product of the same
                 // BN/2 result columns
                 for (int c = side * (half_cols / 2); c < (side + 1) * (half_cols / 2) && rows_in; c += 32) {
+                    const int col = w.nt * half_cols + c;
+                    if (col >= p.o.cols) break;
                     float g[32], v[32];
                     load(c, g);
                     load(half_cols + c, v);
-                    const int col = w.nt * half_cols + c;
-                    if (r >= p.o.rows || col >= p.o.cols) continue;
                     if (p.o.G) {
-                        store32(p.o.G + (size_t)r * p.o.ldg, col, p.o.cols, p.o.vec & 4, g);
-                        store32(p.o.U + (size_t)r * p.o.ldu, col, p.o.cols, p.o.vec & 8, v);
+                        store_block(stage, lane, p.o.G, p.o.ldg, nullptr, 0, r0, p.o.rows, col, p.o.cols, p.o.vec & 4, p.o.vec & 32, g);
+                        store_block(stage, lane, p.o.U, p.o.ldu, nullptr, 0, r0, p.o.rows, col, p.o.cols, p.o.vec & 8, p.o.vec & 64, v);
                     }
 #pragma unroll
                     for (int j = 0; j < 32; j++) v[j] *= act_f32(g[j], p.o.act);
-                    store32(p.o.Y + (size_t)r * p.o.ldy, col, p.o.cols, p.o.vec & 1, v);
+                    store_block(stage, lane, p.o.Y, p.o.ldy, nullptr, 0, r0, p.o.rows, col, p.o.cols, p.o.vec & 1, p.o.vec & 16, v);
                 }
             } else {
                 // Packed gradient: row r of the weight is bit r % 64 of its strip's words; a
@@ -730,7 +791,7 @@ int gemm_pairs() {
 struct GemmPlan {
     int m_tiles, n_tiles, problems, BN, parts, n_whole, stages;
     long long tiles, n_units;
-    uint32_t block_bytes, stage_bytes, off_bar;
+    uint32_t block_bytes, stage_bytes, off_bar, off_stage;
     size_t smem;
     uint64_t counter_bytes, partial_bytes;
     double cost;  // microseconds
@@ -772,10 +833,12 @@ int plan_gemm(long long rows, long long cols, int problems, long long ksteps, in
     g->block_bytes = kABytes + (uint32_t)g->BN / 2 * 128;
     g->stage_bytes = 2 * g->block_bytes;
     const uint32_t bars = 8u * (2 * kMaxStages + 5) + 32u;
-    g->stages = (int)((kSmemLimit - 1024 - bars) / g->stage_bytes);
+    const uint32_t blocks = 4u * kEpiWarps * 32 * 33;
+    g->stages = (int)((kSmemLimit - 1024 - bars - blocks) / g->stage_bytes);
     if (g->stages > kMaxStages) g->stages = kMaxStages;
     g->off_bar = (uint32_t)g->stages * g->stage_bytes;
-    g->smem = (size_t)g->off_bar + bars + 1024;
+    g->off_stage = g->off_bar + (uint32_t)round_up_u64(bars, 16);
+    g->smem = (size_t)g->off_stage + blocks + 1024;
     return SPW_OK;
 }
 
@@ -794,6 +857,7 @@ void fill_params(const GemmPlan& g, long long ksteps, GemmParams* p) {
     p->block_bytes = g.block_bytes;
     p->stage_bytes = g.stage_bytes;
     p->off_bar = g.off_bar;
+    p->off_stage = g.off_stage;
     p->wait_limit = wait_limit_cycles();
     p->status = device_status_ptr();
 }
@@ -868,6 +932,14 @@ uint64_t map_ld(int ld, int rows) { return 2ull * (rows > 1 ? (uint64_t)ld : rou
 
 bool vec_ok(const void* p, int ld) { return !p || (ld % 8 == 0 && aligned16(p)); }
 
+// PrefillOut::vec from the leading dimensions (every pointer is 16-byte aligned).
+int vec_bits(const PrefillOut& o) {
+    const bool even_r = !o.residual || o.ldr % 2 == 0;
+    return (vec_ok(o.Y, o.ldy) ? 1 : 0) | (vec_ok(o.residual, o.ldr) ? 2 : 0) | (vec_ok(o.G, o.ldg) ? 4 : 0) |
+           (vec_ok(o.U, o.ldu) ? 8 : 0) | (o.ldy % 2 == 0 && even_r ? 16 : 0) | (o.ldg % 2 == 0 ? 32 : 0) |
+           (o.ldu % 2 == 0 ? 64 : 0);
+}
+
 // Workspace sections: the split counters of each product, the expanded weights, dG and dU
 // where there are any, and the fp32 partials (shared by the products, which run in turn).
 struct Layout {
@@ -879,12 +951,13 @@ struct Layout {
 
 constexpr int kForward = 1, kDxOut = 2, kDvOut = 4;
 
-// Whether the direct form takes less time than expansion and product.  Expansion reads the
-// compressed weight and writes 2 bytes an entry: about 3.1 bytes an entry at 5.2 TB/s, after
-// 4 us, and the clearing of counters another 2.
+// Whether the direct form takes less time than expansion and product.  Measured: the expansion
+// takes 3.5 us and 0.53 us for a million entries, the product 3 us beside its units, and the
+// clearing of counters 2.  (4096 x 4096: direct / expanded 25 / 29 us at 256 tokens, 36 / 31 at
+// 512; 11008 x 4096: 60 / 62 and 84 / 81.)
 bool choose_direct(int mode, const spw_format* h, const spw_format* h2, int M, const GemmPlan& g) {
     const double entries = (h2 ? 2.0 : 1.0) * h->n_strips * (double)h->n_ktiles * kStripRows * kTileCols;
-    const double other = g.cost + 4.0 + entries * 3.1 / 5.2e6 + (g.counter_bytes ? 2.0 : 0.0);
+    const double other = g.cost + 6.5 + entries * 0.53e-6 + (g.counter_bytes ? 2.0 : 0.0);
     const double direct = direct_cost(mode, h, h2, M);
     return direct >= 0.0 && direct <= other;
 }
@@ -996,7 +1069,7 @@ int run_dx(const spw_format* const* hdrs, const void* const* bufs, int weights, 
     o.cols = (int)h->K;
     o.Y = dX;
     o.ldy = lddx;
-    o.vec = vec_ok(dX, lddx) ? 1 : 0;
+    o.vec = vec_bits(o);
     if (L.dx_direct) {
         DirectCall c;
         memset(&c, 0, sizeof(c));
@@ -1119,7 +1192,7 @@ int spw_spmm_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_X, i
         o.residual = ep->residual;
         o.ldr = ep->ldr;
     }
-    o.vec = (vec_ok(d_Y, ldy) ? 1 : 0) | (vec_ok(o.residual, o.ldr) ? 2 : 0);
+    o.vec = vec_bits(o);
     return run_forward<kEp>(L, &hdr, &d_buf, d_X, M, ldx, o, (uint8_t*)d_ws, s);
 }
 
@@ -1166,7 +1239,7 @@ int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_f
     o.U = d_U;
     o.ldu = ldu;
     o.act = act;
-    o.vec = (vec_ok(d_H, ldh) ? 1 : 0) | (vec_ok(d_G, ldg) ? 4 : 0) | (vec_ok(d_U, ldu) ? 8 : 0);
+    o.vec = vec_bits(o);
     const spw_format* hdrs[2] = {hdr_gate, hdr_up};
     const void* bufs[2] = {d_buf_gate, d_buf_up};
     return run_forward<kFfn>(L, hdrs, bufs, d_X, M, ldx, o, (uint8_t*)d_ws, s);

@@ -42,7 +42,6 @@ constexpr int kSmemLimit = 227 * 1024;
 constexpr int kFirstDecoder = 3;
 constexpr int kMaxParts = 8;
 constexpr int kMaxTok = 512;
-constexpr int kChunk = 128;                  // tokens that go through shared memory at a time
 
 __host__ __device__ constexpr int threads_of(int groups) { return 32 * (kFirstDecoder + 4 * groups); }
 
@@ -61,6 +60,7 @@ struct DirectParams {
     int parts, m_tiles, MT, nh; // nh MMAs of MT / nh tokens a slice
     int n_acc;                  // accumulators: 4 for few tokens, where a chain of MMAs waits for its own results
     int sx, sw, sr;             // slots of token tiles, dense tiles, compressed tiles
+    int chunk;                  // tokens of the result that shared memory holds at a time
     uint32_t x_bytes, val_slot, raw_bytes, tmem_cols;
     uint32_t off_w, off_raw, off_rec, off_bar;
     int* status;
@@ -384,12 +384,12 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
     __syncthreads();
 
     // ---------------------------------------------------------------- result
-    // kChunk tokens at a time: every CTA of the cluster puts its piece into its shared memory
+    // p.chunk tokens at a time: every CTA of the cluster puts its piece into its shared memory
     // ([token][128 rows], over the slots, which are no longer in use), then adds the pieces of its
     // share of the tokens and writes them.  (After an abort the values mean nothing.)
     float* buf = (float*)smem;
-    for (int c0 = 0; c0 < p.MT; c0 += kChunk) {
-        const int n = min(kChunk, p.MT - c0);
+    for (int c0 = 0; c0 < p.MT; c0 += p.chunk) {
+        const int n = min(p.chunk, p.MT - c0);
         if (warp >= kFirstDecoder) {
             const int d = warp - kFirstDecoder, quarter = warp & 3;
             for (int c = 32 * (d >> 2); c < n; c += 32 * GROUPS) {
@@ -477,7 +477,7 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
 
 // ------------------------------------------------------------------ host side
 struct DirectPlan {
-    int groups, parts, wt, m_tiles, MT, nh, n_acc, steps, sx, sw, sr;
+    int groups, parts, wt, m_tiles, MT, nh, n_acc, steps, sx, sw, sr, chunk;
     uint32_t x_bytes, val_slot, raw_bytes, tmem_cols, off_w, off_raw, off_rec, off_bar;
     size_t smem;
     double cost;
@@ -497,8 +497,9 @@ bool fit(DirectPlan* g, uint32_t limit) {
         g->off_raw = g->off_w + (uint32_t)g->sw * kWBytes;
         g->off_rec = g->off_raw + (uint32_t)g->sr * g->raw_bytes;
         g->off_bar = g->off_rec + kRecBytes * 4u * (uint32_t)g->groups;
-        const uint32_t stage = (uint32_t)(g->MT < kChunk ? g->MT : kChunk) * 512u;  // the result's way out
-        if (g->off_rec < stage) continue;
+        g->chunk = (int)(g->off_rec / 512u) / 32 * 32;  // over the slots
+        if (g->chunk > g->MT) g->chunk = g->MT;
+        if (g->chunk < 16) continue;
         g->smem = (size_t)g->off_bar + kBarBytes + 1024;
         if (g->smem <= limit) return true;
     }
@@ -576,10 +577,14 @@ int plan_direct(int mode, const spw_format* h, const spw_format* h2, int M, Dire
                 if (slots <= 0) continue;
                 const double waves = (double)((tiles * parts + slots - 1) / slots);
                 const double steps = (double)((g.steps + parts - 1) / parts);
-                // a step of two tiles: the decoding, or shared memory's share of the tokens
-                double step = 0.36 > 0.15 + 0.85 * g.MT / 512.0 ? 0.36 : 0.15 + 0.85 * g.MT / 512.0;
-                if (groups == 2) step *= 1.9;
-                const double cost = waves * (steps * step + (groups == 2 ? 3.5 : 4.5) + 0.4 * (parts > 1) + 0.008 * g.MT);
+                // Measured: a step of two tiles (decoding, and shared memory's share of the tokens);
+                // what a CTA takes before the first and after the last, most of it the exchange of
+                // the pieces.  (4096 x 4096, 4 pieces of 16 steps: 16.4 us at 16 tokens, 19.3 at 128,
+                // 23.5 at 256, 32.8 at 512.)  Two CTAs on an SM slow each other down, but the one
+                // works while the other starts or ends: 11008 x 4096 at 16 tokens 34 us against 39.
+                const double step = groups == 4 ? 0.58 + 0.00056 * g.MT
+                                                : (tiles * parts > device_sm_count() ? 1.2 : 0.8) + 0.0026 * g.MT;
+                const double cost = waves * (steps * step + 6.1 + (parts > 1 ? 0.8 + 0.0235 * g.MT : 0.008 * g.MT));
                 if (best->cost < 0 || cost < best->cost * 0.98) {
                     *best = g;
                     best->parts = parts;
@@ -634,6 +639,7 @@ int direct_launch(const DirectCall& c, cudaStream_t s) {
     p.sx = g.sx;
     p.sw = g.sw;
     p.sr = g.sr;
+    p.chunk = g.chunk;
     p.x_bytes = g.x_bytes;
     p.val_slot = g.val_slot;
     p.raw_bytes = g.raw_bytes;

@@ -19,7 +19,8 @@ struct PrefillOut {
     uint16_t* G;
     uint16_t* U;
     int ldy, ldr, ldg, ldu, act;
-    int vec;         // bit 0: Y, 1: residual, 2: G, 3: U take 16-byte accesses
+    int vec;         // bit 0: Y, 1: residual, 2: G, 3: U take 16-byte accesses;
+                     // 4: Y and residual, 5: G, 6: U take 4-byte ones
     int rows, cols;  // of the result (kFfn: of H)
 };
 
