@@ -163,8 +163,9 @@ def _check(fn: str, status: int):
 
 
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is None:  # the handle alone: building a Stream object costs 3 us a call
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def _ptr(t: torch.Tensor | None):
@@ -775,18 +776,20 @@ def _act(act) -> int:
     return int(act)
 
 
-def _same_device(first: torch.Tensor, **tensors):
+def _same_device(*tensors):
     """The library works on the current device: every tensor has to live there."""
     dev = torch.cuda.current_device()
-    for name, t in {"the input": first, **tensors}.items():
-        if t is not None and (not t.is_cuda or t.device.index != dev):
-            raise ValueError(f"{name} is on {t.device}; the current CUDA device is cuda:{dev}")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor of shape {tuple(t.shape)} is on {t.device}; the current CUDA "
+                             f"device is cuda:{dev}")
 
 
 def _out(t: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, name: str):
     """An fp16 output of at least rows x cols (allocated when not given): (tensor, view, ld)."""
     if t is None:
         t = torch.empty((rows, cols), dtype=torch.float16, device=like.device)
+        return t, t, cols
     v, ld = _rows(_half(t, name), name)
     _need(v, rows, cols, name)
     return t, v, ld
@@ -823,14 +826,16 @@ def _packed(t: torch.Tensor | None, h, like: torch.Tensor, name: str) -> torch.T
     return t
 
 
-def _packed_ptr(dv: torch.Tensor | None, ws: torch.Tensor):
+def _packed_ptr(dv: torch.Tensor | None, buf: torch.Tensor):
     """The pointer of a packed gradient.  That of a weight with nothing kept is empty, and an
-    empty tensor has no address: any aligned one stands for it, nothing is written there."""
-    return _ptr(ws) if dv is not None and dv.numel() == 0 else _ptr(dv)
+    empty tensor has no address: the end of the weight's buffer, where its empty values section
+    is, stands for it; nothing is written there."""
+    return _ptr(buf) if dv is not None and dv.numel() == 0 else _ptr(dv)
 
 
-def _ws_of(ws: torch.Tensor | None, need: int, like: torch.Tensor) -> torch.Tensor:
-    return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device) if ws is None else ws
+def _ws_of(ws: torch.Tensor | None, need: int, like: torch.Tensor) -> torch.Tensor | None:
+    """The caller's workspace, or one of `need` bytes (none for 0)."""
+    return torch.empty(need, dtype=torch.uint8, device=like.device) if ws is None and need else ws
 
 
 def _epilogue(bias, act, residual, rows: int, N: int) -> spw_epilogue:
@@ -857,7 +862,7 @@ def spw_spmv_ep(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
     number; the rest as spw_spmv, whose workspace this call uses."""
     h = _hdr(hdr)
     x2, B, ldx = _x_of(x, h.K, "x")
-    _same_device(x, buf=buf, act_bits=act_bits, bias=bias, residual=residual, y=y, ws=ws)
+    _same_device(x, buf, act_bits, bias, residual, y, ws)
     ep = _epilogue(bias, act, residual, B, h.N)
     _need_buf(buf, h)
     _need_words(act_bits, h.K)
@@ -884,7 +889,7 @@ def spw_spmm_ep(hdr, buf: torch.Tensor, X: torch.Tensor, bias: torch.Tensor | No
     any content (allocated here when not given)."""
     h = _hdr(hdr)
     X2, M, ldx = _x_of(X, h.K, "X")
-    _same_device(X, buf=buf, bias=bias, residual=residual, Y=Y, ws=ws)
+    _same_device(X, buf, bias, residual, Y, ws)
     ep = _epilogue(bias, act, residual, M, h.N)
     _need_buf(buf, h)
     Y, Y2, ldy = _out(Y, M, h.N, X, "Y")
@@ -913,7 +918,7 @@ def spw_spmm_ffn(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor,
     if (G is None) != (U is None):
         raise ValueError("G and U go together")
     save = save or G is not None
-    _same_device(X, buf_gate=buf_gate, buf_up=buf_up, H=H, G=G, U=U, ws=ws)
+    _same_device(X, buf_gate, buf_up, H, G, U, ws)
     _need_buf(buf_gate, hg, "buf_gate")
     _need_buf(buf_up, hu, "buf_up")
     H, H2, ldh = _out(H, M, hg.N, X, "H")
@@ -954,8 +959,7 @@ def spw_spmm_ffn_backward(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torc
     if need_dv and X is None:
         raise ValueError("the weights' gradients need X")
     X2, ldx = _in(X, M, hg.K, "X") if X is not None else (None, 0)
-    _same_device(G, U=U, dH=dH, X=X, buf_gate=buf_gate, buf_up=buf_up, dX=dX, dV_gate=dV_gate,
-                 dV_up=dV_up, ws=ws)
+    _same_device(G, U, dH, X, buf_gate, buf_up, dX, dV_gate, dV_up, ws)
     _need_buf(buf_gate, hg, "buf_gate")
     _need_buf(buf_up, hu, "buf_up")
     dX2, lddx = None, 0
@@ -968,8 +972,8 @@ def spw_spmm_ffn_backward(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torc
     ws = _ws_of(ws, spw_spmm_ffn_backward_workspace_bytes(hg, hu, M), G)
     _check("spw_spmm_ffn_backward", lib().spw_spmm_ffn_backward(
         ctypes.byref(hg), _ptr(buf_gate), ctypes.byref(hu), _ptr(buf_up), _ptr(X2), M, ldx, _act(act),
-        _ptr(G2), ldg, _ptr(U2), ldu, _ptr(dH2), lddh, _ptr(dX2), lddx, _packed_ptr(dV_gate, ws),
-        _packed_ptr(dV_up, ws), _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(G2), ldg, _ptr(U2), ldu, _ptr(dH2), lddh, _ptr(dX2), lddx, _packed_ptr(dV_gate, buf_gate),
+        _packed_ptr(dV_up, buf_up), _ptr(ws), _nbytes(ws), _stream(stream)))
     return dX, dV_gate, dV_up
 
 
@@ -987,7 +991,7 @@ def spw_spmm_backward(hdr, buf: torch.Tensor, X: torch.Tensor | None, dY: torch.
     if need_dv and X is None:
         raise ValueError("the weight's gradient needs X")
     X2, ldx = _in(X, M, h.K, "X") if X is not None else (None, 0)
-    _same_device(dY, X=X, buf=buf, dX=dX, dV=dV, ws=ws)
+    _same_device(dY, X, buf, dX, dV, ws)
     _need_buf(buf, h)
     dX2, lddx = None, 0
     if need_dx:
@@ -998,7 +1002,7 @@ def spw_spmm_backward(hdr, buf: torch.Tensor, X: torch.Tensor | None, dY: torch.
     ws = _ws_of(ws, spw_spmm_backward_workspace_bytes(h, M), dY)
     _check("spw_spmm_backward", lib().spw_spmm_backward(
         ctypes.byref(h), _ptr(buf), _ptr(X2), M, ldx, _ptr(dY2), lddy, _ptr(dX2), lddx,
-        _packed_ptr(dV, ws), _ptr(ws), _nbytes(ws), _stream(stream)))
+        _packed_ptr(dV, buf), _ptr(ws), _nbytes(ws), _stream(stream)))
     return dX, dV
 
 

@@ -548,8 +548,7 @@ int resident(int groups, int parts) {
     return n;
 }
 
-int plan_direct(int mode, const spw_format* h, const spw_format* h2, int M, DirectPlan* best) {
-    const uint32_t units = h2 && h2->max_tile_units > h->max_tile_units ? h2->max_tile_units : h->max_tile_units;
+int search_plan(int mode, const spw_format* h, const spw_format* h2, int M, uint32_t units, DirectPlan* best) {
     best->cost = -1.0;
     for (int groups = 2; groups <= 4; groups += 2)
         for (int cap = kMaxTok; cap >= 64; cap /= 2) {
@@ -593,6 +592,43 @@ int plan_direct(int mode, const spw_format* h, const spw_format* h2, int M, Dire
             }
         }
     return best->cost < 0 ? SPW_ERR_UNSUPPORTED : SPW_OK;
+}
+
+// A call asks for its plan up to three times (workspace, choice, launch): the thread's last
+// plans are kept by what they follow from.
+int plan_direct(int mode, const spw_format* h, const spw_format* h2, int M, DirectPlan* out) {
+    struct Key {
+        int dev, mode, weights, M;
+        uint32_t N, K, units;
+    };
+    struct Entry {
+        Key key;
+        DirectPlan plan;
+        int rc;
+        bool used;
+    };
+    static thread_local Entry cache[4];
+    static thread_local unsigned turn;
+    Key key;
+    memset(&key, 0, sizeof(key));
+    if (cudaGetDevice(&key.dev) != cudaSuccess) return SPW_ERR_CUDA;
+    key.mode = mode;
+    key.weights = h2 ? 2 : 1;
+    key.M = M;
+    key.N = h->N;
+    key.K = h->K;
+    key.units = h2 && h2->max_tile_units > h->max_tile_units ? h2->max_tile_units : h->max_tile_units;
+    for (Entry& e : cache)
+        if (e.used && memcmp(&e.key, &key, sizeof(key)) == 0) {
+            *out = e.plan;
+            return e.rc;
+        }
+    Entry& e = cache[turn++ % 4];
+    e.key = key;
+    e.rc = search_plan(mode, h, h2, M, key.units, &e.plan);
+    e.used = true;
+    *out = e.plan;
+    return e.rc;
 }
 
 }  // namespace
