@@ -497,25 +497,35 @@ typedef struct {
     int32_t act; /* spw_activation */
 } spw_epilogue;
 
-/* Decode with an epilogue, for 1 to 16 rows: the product is spw_spmv's (same threshold
- * rule, column set, workspace and its rules, determinism; a dropped weight or column
- * never touches the sum), the epilogue as above.  Asynchronous.  Errors: as spw_spmv,
- * plus INVALID_ARG (unknown act, ldr < N) and ALIGNMENT for the epilogue's pointers. */
+/* Decode with an epilogue, for 1 to 16 rows: the product is spw_spmv's (same arguments,
+ * threshold rule and column set), the epilogue as above.  Two paths, chosen on the host by
+ * shape and batch: the CUDA-core decode of spw_spmv for the fewest rows, the tensor-core
+ * kernel of spw_spmm_ep with the rule applied to x from where it measured faster (3 to 6
+ * rows).  On the tensor-core path a non-finite x~ entry reaches every output, also through
+ * weights that the mask drops (as in spw_spmv_tc).  Deterministic.  Asynchronous.
+ *   spw_spmv_ep_path(hdr, B): 0 (CUDA cores), 1 (tensor cores), -1 (invalid header or B).
+ *   spw_spmv_ep_workspace_bytes(hdr, B): 0 on the tensor-core path (d_ws may be NULL), else
+ *   spw_spmv's workspace with its rules (counters zero before the first call, left zero).
+ * Errors: as spw_spmv, plus INVALID_ARG (unknown act, ldr < N) and ALIGNMENT for the
+ * epilogue's pointers. */
+int spw_spmv_ep_path(const spw_format* hdr, int B);
+uint64_t spw_spmv_ep_workspace_bytes(const spw_format* hdr, int B);
 int spw_spmv_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, int B, int ldx,
                 float threshold, const uint32_t* d_act_bits, const spw_epilogue* ep, uint16_t* d_y,
                 int ldy, void* d_ws, uint64_t ws_bytes, void* stream);
 
-/* Prefill with an epilogue: Y = act(X W_masked^T + bias) + residual for M rows.  The
- * weight is expanded to dense fp16 in the workspace and multiplied on tcgen05 SM pairs,
- * so the workspace is at least 2 N K bytes (rows and columns rounded up to 64).  A
- * dropped weight is an explicit zero there, so a non-finite X entry reaches every column
- * of its row, as in spw_spmm.  M >= 0 (M == 0 does nothing).
- * Workspace of this call and of the three below: spw_..._workspace_bytes(..., M) bytes,
- * 16-byte aligned, of any content; nothing is kept in it between calls.  Calls that may run
- * at the same time must not share one.  Deterministic.  Asynchronous.  Errors: INVALID_ARG,
- * ALIGNMENT, FORMAT, BUFFER_TOO_SMALL, UNSUPPORTED (too many tiles), CUDA; device timeouts
- * as for spw_spmv.  A tile that disagrees with its header counts as empty (FORMAT through
- * spw_last_device_status). */
+/* Prefill with an epilogue: Y = act(X W_masked^T + bias) + residual for M rows, on tcgen05
+ * tensor cores.  Two forms, chosen on the host by shape and M where they measured faster: for
+ * few rows the compressed weight is decoded into shared memory; for many it is first expanded
+ * to dense fp16 in the workspace (at least 2 N K bytes then, rows and columns rounded up).  A
+ * dropped weight is an explicit zero in both, so a non-finite X entry reaches every column of
+ * its row, as in spw_spmm.  M >= 0 (M == 0 does nothing).
+ * Workspace of this call and of the three below: spw_..._workspace_bytes(..., M) bytes (0: d_ws
+ * may be NULL), 16-byte aligned, of any content; nothing is kept in it between calls.  Calls
+ * that may run at the same time must not share one.  Deterministic.  Asynchronous.  Errors:
+ * INVALID_ARG, ALIGNMENT, FORMAT, BUFFER_TOO_SMALL, UNSUPPORTED (too many tiles), CUDA; device
+ * timeouts as for spw_spmv.  A tile that disagrees with its header counts as empty (FORMAT
+ * through spw_last_device_status). */
 uint64_t spw_spmm_ep_workspace_bytes(const spw_format* hdr, int M);
 int spw_spmm_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_X, int M, int ldx,
                 const spw_epilogue* ep, uint16_t* d_Y, int ldy, void* d_ws, uint64_t ws_bytes,

@@ -115,6 +115,8 @@ SIGNATURES = {
     "spw_spmm24_workspace_bytes": ([_FP, _I], _U64),
     "spw_spmm24_plan": ([_FP, _I, _I, ctypes.POINTER(spw_spmm_plan_info)], _I),
     "spw_spmm24": ([_FP, _P, _P, _U64, _P, _I, _I, _P, _I, _P, _U64, _P], _I),
+    "spw_spmv_ep_path": ([_FP, _I], _I),
+    "spw_spmv_ep_workspace_bytes": ([_FP, _I], _U64),
     "spw_spmv_ep": ([_FP, _P, _P, _I, _I, _F, _P, _EP, _P, _I, _P, _U64, _P], _I),
     "spw_spmm_ep_workspace_bytes": ([_FP, _I], _U64),
     "spw_spmm_ep": ([_FP, _P, _P, _I, _I, _EP, _P, _I, _P, _U64, _P], _I),
@@ -851,6 +853,16 @@ def _epilogue(bias, act, residual, rows: int, N: int) -> spw_epilogue:
     return ep
 
 
+def spw_spmv_ep_path(hdr, B: int) -> int:
+    """0 when spw_spmv_ep takes the CUDA-core decode for this weight and batch, 1 for the tensor
+    cores, -1 for B outside 1..16."""
+    return int(lib().spw_spmv_ep_path(ctypes.byref(_hdr(hdr)), int(B)))
+
+
+def spw_spmv_ep_workspace_bytes(hdr, B: int) -> int:
+    return int(lib().spw_spmv_ep_workspace_bytes(ctypes.byref(_hdr(hdr)), int(B)))
+
+
 def spw_spmv_ep(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
                 act_bits: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                 act=SPW_ACT_NONE, residual: torch.Tensor | None = None,
@@ -859,7 +871,8 @@ def spw_spmv_ep(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
     """Decode with an epilogue: y = act(W_masked . x~ + bias) + residual (B x N fp16, B <= 16).
 
     bias: N fp16; residual: B x N fp16 (it may be y itself); act: a name of ACTIVATIONS or its
-    number; the rest as spw_spmv, whose workspace this call uses."""
+    number; the rest as spw_spmv.  ws: a zero-initialised uint8 workspace of
+    spw_spmv_ep_workspace_bytes(hdr, B) bytes (allocated here when needed and not given)."""
     h = _hdr(hdr)
     x2, B, ldx = _x_of(x, h.K, "x")
     _same_device(x, buf, act_bits, bias, residual, y, ws)
@@ -868,7 +881,8 @@ def spw_spmv_ep(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
     _need_words(act_bits, h.K)
     y, y2, ldy = _out(y, B, h.N, x, "y")
     if ws is None:
-        ws = torch.zeros(max(spw_spmv_workspace_bytes(h, B), 16), dtype=torch.uint8, device=x.device)
+        need = spw_spmv_ep_workspace_bytes(h, B)
+        ws = torch.zeros(need, dtype=torch.uint8, device=x.device) if need else None
     _check("spw_spmv_ep", lib().spw_spmv_ep(
         ctypes.byref(h), _ptr(buf), _ptr(x2), B, ldx, float(threshold), _ptr(act_bits),
         ctypes.byref(ep), _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream(stream)))
@@ -1057,8 +1071,12 @@ class SparseLinear:
     def spmv_ep(self, x, threshold=0.0, act_bits=None, bias=None, act=SPW_ACT_NONE, residual=None,
                 y=None, stream=None):
         x2 = x if x.dim() == 2 else x.unsqueeze(0)
+        B = x2.shape[0]
+        if ("ep", B) not in self._ws:
+            need = spw_spmv_ep_workspace_bytes(self.hdr, B)
+            self._ws[("ep", B)] = torch.zeros(need, dtype=torch.uint8, device=self.buf.device) if need else None
         return spw_spmv_ep(self.hdr, self.buf, x2, threshold, act_bits, bias, act, residual, y,
-                           self.workspace(x2.shape[0]), stream)
+                           self._ws[("ep", B)], stream)
 
     def spmm_ep(self, X, bias=None, act=SPW_ACT_NONE, residual=None, Y=None, ws=None, stream=None):
         return spw_spmm_ep(self.hdr, self.buf, X, bias, act, residual, Y, ws, stream)

@@ -930,15 +930,6 @@ int expand(int n, const spw_format* const* hdrs, const void* const* bufs, uint16
 // Row stride in bytes for a tensor map: a single row may have any leading dimension.
 uint64_t map_ld(int ld, int rows) { return 2ull * (rows > 1 ? (uint64_t)ld : round_up_u64((uint64_t)ld, 8)); }
 
-bool vec_ok(const void* p, int ld) { return !p || (ld % 8 == 0 && aligned16(p)); }
-
-// PrefillOut::vec from the leading dimensions (every pointer is 16-byte aligned).
-int vec_bits(const PrefillOut& o) {
-    const bool even_r = !o.residual || o.ldr % 2 == 0;
-    return (vec_ok(o.Y, o.ldy) ? 1 : 0) | (vec_ok(o.residual, o.ldr) ? 2 : 0) | (vec_ok(o.G, o.ldg) ? 4 : 0) |
-           (vec_ok(o.U, o.ldu) ? 8 : 0) | (o.ldy % 2 == 0 && even_r ? 16 : 0) | (o.ldg % 2 == 0 ? 32 : 0) |
-           (o.ldu % 2 == 0 ? 64 : 0);
-}
 
 // Workspace sections: the split counters of each product, the expanded weights, dG and dU
 // where there are any, and the fp32 partials (shared by the products, which run in turn).
@@ -1144,6 +1135,13 @@ int run_dv(const spw_format* const* hdrs, const void* const* bufs, int weights, 
 
 }  // namespace
 
+int vec_bits(const PrefillOut& o) {
+    auto ok = [](const void* p, int ld) { return !p || ld % 8 == 0; };
+    return (ok(o.Y, o.ldy) ? 1 : 0) | (ok(o.residual, o.ldr) ? 2 : 0) | (ok(o.G, o.ldg) ? 4 : 0) | (ok(o.U, o.ldu) ? 8 : 0) |
+           (o.ldy % 2 == 0 && (!o.residual || o.ldr % 2 == 0) ? 16 : 0) | (o.ldg % 2 == 0 ? 32 : 0) |
+           (o.ldu % 2 == 0 ? 64 : 0);
+}
+
 // Checks of an epilogue's arguments for a result of N columns.
 int check_epilogue(const spw_epilogue* ep, int N) {
     if (!ep) return SPW_OK;
@@ -1288,7 +1286,7 @@ int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate, co
     const long long most = 16ll * device_sm_count();
     if (most <= 0) return SPW_ERR_CUDA;
     const long long grid = (n + 255) / 256 < most ? (n + 255) / 256 : most;
-    const int vec = vec_ok(d_G, ldg) && vec_ok(d_U, ldu) && vec_ok(d_dH, lddh) ? 1 : 0;
+    const int vec = ldg % 8 == 0 && ldu % 8 == 0 && lddh % 8 == 0 ? 1 : 0;
     if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
     gate_grad_kernel<<<(unsigned)grid, 256, 0, s>>>(d_G, ldg, d_U, ldu, d_dH, lddh, M, N, act, vec, dG, dU, L.ldn);
     SPW_LAUNCH_CHECK();

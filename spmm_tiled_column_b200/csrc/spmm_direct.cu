@@ -4,6 +4,7 @@
 //   kEp   Y = act(X W^T + bias) + residual     A = 128 weight rows (two strips)
 //   kFfn  H = act(X Wg^T) * (X Wu^T)           A = 64 gate rows, then the same 64 up rows
 //   kDx   dX = sum over the weights of dY W    A = 128 weight columns (two k-tiles), MN-major
+//   kDecode  as kEp for at most 16 rows, with the decode's threshold rule and column set
 //
 // With few tokens each weight tile is needed once or twice, so what bounds the product is the
 // decoding (about 900 warp instructions and 300 shared-memory wavefronts for a 64 x 64 tile)
@@ -17,7 +18,8 @@
 //     own, a warp on 32 columns of one tile: the waits, scans and look-ups of the groups
 //     overlap.  A step's dense tiles are stored as core matrices of 8 rows x 16 bytes (no
 //     swizzle), which the MMA takes K-major (kEp, kFfn) or MN-major (kDx) from the same bytes.
-//   * warp 0: TMA of the token tiles; warp 1: MMAs; warp 2: tile pointers (16 steps at a time,
+//   * warp 0: TMA of the token tiles (kDecode: loads them itself and applies the rule on the
+//     way into shared memory); warp 1: MMAs; warp 2: tile pointers (16 steps at a time,
 //     ahead) and bulk copies of the compressed tiles; warps 3..: decoders.
 //   * The result goes through shared memory, so a warp stores whole rows of 128 (kFfn: 64)
 //     neighbouring columns.
@@ -65,6 +67,11 @@ struct DirectParams {
     uint32_t off_w, off_raw, off_rec, off_bar;
     int* status;
     long long wait_limit;
+    // kDecode: the rows, the rule
+    const uint16_t* x;
+    const uint32_t* act_bits;
+    int B, K, ldx;
+    uint32_t t_bits;  // magnitude bits of the smallest fp16 not below the threshold, at least 1
 };
 
 __device__ inline uint64_t desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
@@ -195,7 +202,7 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
         u1 = __ldg(at + 1);
     };
     if (warp == 2) pointers(0);
-    if (warp == 0 && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tx0) : "memory");
+    if (MODE != kDecode && warp == 0 && lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&tx0) : "memory");
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -204,7 +211,61 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
 
     int x_issued = 0, r_issued = 0;
     if (warp == 0) {
-        if (lane == 0) {  // ------------------------------------------ token tiles
+        if constexpr (MODE == kDecode) {
+            // Rows with the rule applied, written where TMA would put them (128-byte swizzle).  A
+            // lane has four 16-byte chunks of the 16 x 64 tile: rows lane / 8 + 4 i, columns 8 c ..
+            // On fp16 values |v| < t is a comparison of magnitude bits with those of the smallest
+            // fp16 not below t (p.t_bits, at least 1: an exact zero is dropped, NaN is kept).
+            const int c = lane & 7, r0 = lane >> 3;
+            const uint32_t tb = p.t_bits | p.t_bits << 16;
+            const bool ruled = p.t_bits > 1 || p.act_bits;  // else only zeros are dropped
+            uint4 v[4], vn[4];
+            uint32_t on = 0xFFu, on_n = 0xFFu;
+            auto fetch = [&](int k, uint4 (&to)[4], uint32_t& bits) {
+                const int col = kBK * k + 8 * c;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int r = r0 + 4 * i;
+                    to[i] = r < p.B && col < p.K ? __ldg((const uint4*)(p.x + (size_t)r * p.ldx + col)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+                bits = p.act_bits && col < p.K ? __ldg(p.act_bits + (col >> 5)) >> (col & 31) : 0xFFu;
+                if (col + 8 > p.K) bits &= (1u << max(p.K - col, 0)) - 1u;
+            };
+            fetch(k0, v, on);
+            for (int n = 0, slot = 0; n < nk; n++) {
+                if (n + 1 < nk) fetch(k0 + n + 1, vn, on_n);
+                const int last = n - p.sx;
+                if (last >= 0 && !__all_sync(0xffffffffu, wait_or_abort(smem_u32(&x_empty[last % kRing]),
+                                                                        (uint32_t)(last / kRing) & 1u, abort_flag, p.wait_limit))) {
+                    if (lane == 0) flag_abort(abort_flag, p.status);
+                    break;
+                }
+                unsigned char* dst = smem + (uint32_t)slot * p.x_bytes;
+                const bool cut = ruled || kBK * (k0 + n + 1) > p.K;  // warp-uniform
+                uint32_t m[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++)  // columns 2e, 2e+1 of the chunk
+                    m[e] = ((on >> (2 * e)) & 1u ? 0x0000FFFFu : 0u) | ((on >> (2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    if (4 * i >= p.B && n >= p.sx) break;  // rows past the last stay zero
+                    const int r = r0 + 4 * i;
+                    uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    if (cut) {
+#pragma unroll
+                        for (int e = 0; e < 4; e++) w[e] &= m[e] & __vcmpgeu2(w[e] & 0x7FFF7FFFu, tb);
+                    }
+                    *(uint4*)(dst + 128 * r + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();  // generic stores -> tensor-core reads
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&x_full[n % kRing]));
+#pragma unroll
+                for (int i = 0; i < 4; i++) v[i] = vn[i];
+                on = on_n;
+                if (++slot == p.sx) slot = 0;
+            }
+        } else if (lane == 0) {  // --------------------------------- token tiles
             for (int n = 0, slot = 0; n < nk; n++) {
                 const int last = n - p.sx;
                 if (last >= 0 && !wait_or_abort(smem_u32(&x_empty[last % kRing]), (uint32_t)(last / kRing) & 1u, abort_flag,
@@ -444,7 +505,7 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
             } else {
                 const int col = 128 * wt + r;
                 if (col < p.o.cols) {
-                    if constexpr (MODE == kEp) {
+                    if constexpr (MODE == kEp || MODE == kDecode) {
                         if (p.o.bias) add4(p.o.bias, col, p.o.cols, true, v);
 #pragma unroll
                         for (int e = 0; e < 4; e++) v[e] = act_f32(v[e], p.o.act);
@@ -509,8 +570,12 @@ bool fit(DirectPlan* g, uint32_t limit) {
 template <int MODE, int GROUPS>
 const void* kernel_of() { return (const void*)direct_kernel<MODE, GROUPS>; }
 const void* kernel_for(int mode, int groups) {
-    if (groups == 2) return mode == kEp ? kernel_of<kEp, 2>() : mode == kFfn ? kernel_of<kFfn, 2>() : kernel_of<kDx, 2>();
-    return mode == kEp ? kernel_of<kEp, 4>() : mode == kFfn ? kernel_of<kFfn, 4>() : kernel_of<kDx, 4>();
+    switch (mode) {
+        case kEp: return groups == 2 ? kernel_of<kEp, 2>() : kernel_of<kEp, 4>();
+        case kFfn: return groups == 2 ? kernel_of<kFfn, 2>() : kernel_of<kFfn, 4>();
+        case kDx: return groups == 2 ? kernel_of<kDx, 2>() : kernel_of<kDx, 4>();
+        default: return groups == 2 ? kernel_of<kDecode, 2>() : kernel_of<kDecode, 4>();
+    }
 }
 
 // CTAs that can be resident at once in clusters of `parts` (the largest shared memory of the
@@ -524,7 +589,7 @@ int resident(int groups, int parts) {
     int& n = cache[dev][groups == 2][parts];
     if (!n) {
         const int smem = groups == 2 ? kSmemLimit / 2 - 1024 : kSmemLimit;
-        for (int mode = kEp; mode <= kDx; mode++)
+        for (int mode : {kEp, kFfn, kDx, kDecode})
             if (cudaFuncSetAttribute(kernel_for(mode, groups), cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) {
                 (void)cudaGetLastError();
                 return 0;
@@ -612,7 +677,7 @@ int plan_direct(int mode, const spw_format* h, const spw_format* h2, int M, Dire
     Key key;
     memset(&key, 0, sizeof(key));
     if (cudaGetDevice(&key.dev) != cudaSuccess) return SPW_ERR_CUDA;
-    key.mode = mode;
+    key.mode = mode;  // (kDecode plans as kEp)
     key.weights = h2 ? 2 : 1;
     key.M = M;
     key.N = h->N;
@@ -640,7 +705,7 @@ double direct_cost(int mode, const spw_format* h, const spw_format* h2, int M) {
 
 int direct_launch(const DirectCall& c, cudaStream_t s) {
     DirectPlan g;
-    int rc = plan_direct(c.mode, c.h[0], c.h[1], c.M, &g);
+    int rc = plan_direct(c.mode == kDecode ? (int)kEp : c.mode, c.h[0], c.h[1], c.M, &g);
     if (rc != SPW_OK) return rc;
     DirectParams p;
     memset(&p, 0, sizeof(p));
@@ -654,7 +719,9 @@ int direct_launch(const DirectCall& c, cudaStream_t s) {
             p.L[w].values = (const uint16_t*)(buf + h->off_values);
             p.L[w].values_units = (h->bytes_total - h->off_values) / 16;
         }
-        if (c.x[w]) {
+        if (c.mode == kDecode) {
+            memset(&tx[w], 0, sizeof(tx[w]));  // not read
+        } else if (c.x[w]) {
             rc = encode_map_f16(&tx[w], c.x[w], c.mode == kDx ? c.h[0]->N : c.h[0]->K, (uint64_t)c.M, c.ldx_bytes[w], kBK,
                                 (uint32_t)(g.MT / g.nh));
             if (rc != SPW_OK) return rc;
@@ -687,6 +754,20 @@ int direct_launch(const DirectCall& c, cudaStream_t s) {
     p.status = device_status_ptr();
     p.wait_limit = wait_limit_cycles();
     if (!p.status) return SPW_ERR_CUDA;
+    p.x = c.x[0];
+    p.act_bits = c.act_bits;
+    p.B = c.M;
+    p.K = (int)c.h[0]->K;
+    p.ldx = c.ldx;
+    p.t_bits = 1;
+    if (c.mode == kDecode && c.t > 0.0f) {
+        // round up: the nearest fp16, or the next one (the bits of positive fp16 count upward)
+        const __half h = __float2half_rn(c.t);
+        uint16_t bits;
+        memcpy(&bits, &h, 2);
+        if (__half2float(h) < c.t) bits++;
+        p.t_bits = bits < 1 ? 1 : bits;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)((long long)g.wt * g.m_tiles * g.parts));
     cfg.blockDim = dim3((unsigned)threads_of(g.groups));

@@ -43,8 +43,7 @@
 #include <stdlib.h>
 #include <string.h>
 
-#include "spw_act.cuh"
-#include "spw_internal.cuh"
+#include "spw_prefill.cuh"
 
 namespace spw {
 namespace {
@@ -1307,14 +1306,57 @@ int spw_spmv(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, int 
                                d_ws, ws_bytes, (cudaStream_t)stream);
 }
 
+int spw_spmv_ep_path(const spw_format* hdr, int B) {
+    if (check_header(hdr) != SPW_OK || B < 1 || B > 16) return -1;
+    // The CUDA-core decode's time grows with every row, and with the pieces of a strip that its
+    // last warp adds up row by row; the tensor cores' hardly does.  Measured at 50 % (us, 1 / 4 /
+    // 8 rows, against tensor cores): 1000 x 1000 7.0 / 10.5 / 15 against 8.0; 512 x 8192 10 / 21 /
+    // 39 against 17; 4096 x 4096 12 / 19 / 30 against 17; 11008 x 4096 20 / 29 / 43 against 42.
+    const double entries = 1e-6 * (double)hdr->N * hdr->K;
+    double pieces = 2368.0 / hdr->n_strips;
+    if (pieces > hdr->n_ktiles) pieces = hdr->n_ktiles;
+    if (pieces < 1.0) pieces = 1.0;
+    const double cores = (pieces > 1.0 ? 6.4 : 4.6) + 0.3 * entries + 0.02 * pieces +
+                         (B - 1) * ((pieces > 1.0 ? 0.8 : 0.4) + 0.06 * entries + 0.025 * pieces);
+    const double direct = direct_cost(kEp, hdr, nullptr, B);
+    return direct >= 0.0 && direct < cores ? 1 : 0;
+}
+
+uint64_t spw_spmv_ep_workspace_bytes(const spw_format* hdr, int B) {
+    return spw_spmv_ep_path(hdr, B) == 0 ? spw_spmv_workspace_bytes(hdr, B) : 0;
+}
+
 int spw_spmv_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, int B, int ldx,
                 float threshold, const uint32_t* d_act_bits, const spw_epilogue* ep, uint16_t* d_y,
                 int ldy, void* d_ws, uint64_t ws_bytes, void* stream) {
-    if (!hdr) return SPW_ERR_INVALID_ARG;
-    const int rc = check_header(hdr);
+    int rc = check_decode_args(hdr, d_buf, d_x, B, ldx, threshold, d_act_bits, d_y, ldy);
     if (rc != SPW_OK) return rc;
-    const int erc = check_epilogue(ep, (int)hdr->N);
-    if (erc != SPW_OK) return erc;
+    rc = check_epilogue(ep, (int)hdr->N);
+    if (rc != SPW_OK) return rc;
+    if (spw_spmv_ep_path(hdr, B) == 1) {
+        DirectCall c;
+        memset(&c, 0, sizeof(c));
+        c.mode = kDecode;
+        c.h[0] = hdr;
+        c.buf[0] = d_buf;
+        c.x[0] = d_x;
+        c.M = B;
+        c.ldx = ldx;
+        c.t = threshold;
+        c.act_bits = d_act_bits;
+        c.out.rows = B;
+        c.out.cols = (int)hdr->N;
+        c.out.Y = d_y;
+        c.out.ldy = ldy;
+        if (ep) {
+            c.out.bias = ep->bias;
+            c.out.act = ep->act;
+            c.out.residual = ep->residual;
+            c.out.ldr = ep->ldr;
+        }
+        c.out.vec = vec_bits(c.out);
+        return direct_launch(c, (cudaStream_t)stream);
+    }
     return decode_group_launch(1, hdr, &d_buf, &d_x, &ldx, &d_act_bits, &d_y, &ldy, B, threshold,
                                d_ws, ws_bytes, (cudaStream_t)stream, nullptr, ep);
 }

@@ -9,8 +9,9 @@
 namespace spw {
 
 // kEp: act(X W^T + bias) + residual.  kFfn: act(X Wg^T) * (X Wu^T).  kDx: sum of dY W over one
-// or two weights.  kDv: dY^T X at the kept positions (gemm.cu only).
-enum Mode { kEp, kFfn, kDx, kDv };
+// or two weights.  kDv: dY^T X at the kept positions (gemm.cu only).  kDecode: kEp for at most
+// 16 rows with the decode's rule (spmm_direct.cu only).
+enum Mode { kEp, kFfn, kDx, kDv, kDecode };
 
 struct PrefillOut {
     uint16_t* Y;
@@ -34,10 +35,16 @@ struct DirectCall {
     uint64_t ldx_bytes[2];
     int M;
     PrefillOut out;
+    // kDecode: the rows' stride in elements, the threshold and the column set (or null)
+    int ldx;
+    float t;
+    const uint32_t* act_bits;
 };
 
 // Estimated time in microseconds (< 0: the form cannot run this product), and the launch.
 double direct_cost(int mode, const spw_format* h, const spw_format* h2, int M);
+// PrefillOut::vec from its leading dimensions (every pointer is 16-byte aligned).
+int vec_bits(const PrefillOut& o);
 int direct_launch(const DirectCall& c, cudaStream_t s);
 
 // Shared-memory loads of 16 bits, zero-extended (not volatile: see lds_u16).
