@@ -12,6 +12,7 @@ mask as torch.uint8 (nonzero = kept), TCB buffers as torch.uint8, bitmaps as tor
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -787,57 +788,69 @@ def _same_device(*tensors):
                              f"device is cuda:{dev}")
 
 
+def _on_stream(fn):
+    """Gives a call its `stream` keyword.  The call runs with that stream current, so that what
+    it allocates belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _mat(t: torch.Tensor, rows: int | None, cols: int, name: str) -> tuple[torch.Tensor, int, int]:
+    """An fp16 operand of exactly rows x cols (any number of rows for None), unit column
+    stride: (2-D view, rows, leading dimension)."""
+    if t.dtype is not torch.float16:
+        t = _half(t, name)
+    if t.dim() == 1:
+        t = t.unsqueeze(0)
+    if t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
+    m, n = t.shape
+    if n != cols or (rows is not None and m != rows):
+        raise ValueError(f"{name} is {m} x {n}; the call takes {'any' if rows is None else rows} rows of "
+                         f"{cols} columns")
+    return t, m, max(t.stride(0), n)
+
+
 def _out(t: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, name: str):
-    """An fp16 output of at least rows x cols (allocated when not given): (tensor, view, ld)."""
+    """An fp16 output of at least rows x cols (allocated when not given): (tensor, address, ld)."""
     if t is None:
         t = torch.empty((rows, cols), dtype=torch.float16, device=like.device)
-        return t, t, cols
+        return t, t.data_ptr(), cols
     v, ld = _rows(_half(t, name), name)
     _need(v, rows, cols, name)
-    return t, v, ld
-
-
-def _in(t: torch.Tensor, rows: int, cols: int, name: str):
-    """An fp16 operand of exactly rows x cols: (view, ld)."""
-    v, ld = _rows(_half(t, name), name)
-    if tuple(v.shape) != (rows, cols):
-        raise ValueError(f"{name} is {tuple(v.shape)}; the call takes {rows} x {cols}")
-    return v, ld
-
-
-def _x_of(x: torch.Tensor, K: int, name: str):
-    """Rows of activations of exactly K columns: (view, rows, ld)."""
-    v, ld = _rows(_half(x, name), name)
-    if v.shape[1] != K:
-        raise ValueError(f"{name} has {v.shape[1]} columns; the weight has {K}")
-    return v, v.shape[0], ld
+    return t, v.data_ptr(), ld
 
 
 def _values_len(h) -> int:
-    return int(h.bytes_total - h.off_values) // 2
+    return (h.bytes_total - h.off_values) // 2
 
 
-def _packed(t: torch.Tensor | None, h, like: torch.Tensor, name: str) -> torch.Tensor:
-    """A packed gradient: one fp16 entry for each entry of the values section."""
+def _packed(t: torch.Tensor | None, h, buf: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
+    """A packed gradient, one fp16 entry for each entry of the values section, and its address.
+    (That of a weight with nothing kept is empty, and an empty tensor has no address: the
+    weight's buffer stands for it; nothing is written there.)"""
     n = _values_len(h)
     if t is None:
-        return torch.empty(n, dtype=torch.float16, device=like.device)
-    t = _half(t, name)
-    if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1) or t.numel() < n:
-        raise ValueError(f"{name} must be 1-D and contiguous with at least {n} entries")
-    return t
+        t = torch.empty(n, dtype=torch.float16, device=buf.device)
+    else:
+        t = _half(t, name)
+        if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1) or t.numel() < n:
+            raise ValueError(f"{name} must be 1-D and contiguous with at least {n} entries")
+    return t, t.data_ptr() if t.numel() else buf.data_ptr()
 
 
-def _packed_ptr(dv: torch.Tensor | None, buf: torch.Tensor):
-    """The pointer of a packed gradient.  That of a weight with nothing kept is empty, and an
-    empty tensor has no address: the end of the weight's buffer, where its empty values section
-    is, stands for it; nothing is written there."""
-    return _ptr(buf) if dv is not None and dv.numel() == 0 else _ptr(dv)
-
-
-def _ws_of(ws: torch.Tensor | None, need: int, like: torch.Tensor) -> torch.Tensor | None:
-    """The caller's workspace, or one of `need` bytes (none for 0)."""
-    return torch.empty(need, dtype=torch.uint8, device=like.device) if ws is None and need else ws
+def _ws_of(ws: torch.Tensor | None, need: int, like: torch.Tensor):
+    """The caller's workspace, or one of `need` bytes: (tensor, address, bytes)."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+    return ws, ws.data_ptr(), _nbytes(ws)
 
 
 def _epilogue(bias, act, residual, rows: int, N: int) -> spw_epilogue:
@@ -848,7 +861,7 @@ def _epilogue(bias, act, residual, rows: int, N: int) -> spw_epilogue:
             raise ValueError(f"bias must be 1-D and contiguous with {N} entries, got {tuple(b.shape)}")
         ep.bias = b.data_ptr()
     if residual is not None:
-        r, ep.ldr = _in(residual, rows, N, "residual")
+        r, _, ep.ldr = _mat(residual, rows, N, "residual")
         ep.residual = r.data_ptr()
     return ep
 
@@ -863,29 +876,30 @@ def spw_spmv_ep_workspace_bytes(hdr, B: int) -> int:
     return int(lib().spw_spmv_ep_workspace_bytes(ctypes.byref(_hdr(hdr)), int(B)))
 
 
+@_on_stream
 def spw_spmv_ep(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
                 act_bits: torch.Tensor | None = None, bias: torch.Tensor | None = None,
                 act=SPW_ACT_NONE, residual: torch.Tensor | None = None,
-                y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-                stream=None) -> torch.Tensor:
+                y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Decode with an epilogue: y = act(W_masked . x~ + bias) + residual (B x N fp16, B <= 16).
 
     bias: N fp16; residual: B x N fp16 (it may be y itself); act: a name of ACTIVATIONS or its
     number; the rest as spw_spmv.  ws: a zero-initialised uint8 workspace of
     spw_spmv_ep_workspace_bytes(hdr, B) bytes (allocated here when needed and not given)."""
     h = _hdr(hdr)
-    x2, B, ldx = _x_of(x, h.K, "x")
+    x2, B, ldx = _mat(x, None, h.K, "x")
     _same_device(x, buf, act_bits, bias, residual, y, ws)
     ep = _epilogue(bias, act, residual, B, h.N)
     _need_buf(buf, h)
     _need_words(act_bits, h.K)
-    y, y2, ldy = _out(y, B, h.N, x, "y")
+    y, py, ldy = _out(y, B, h.N, x, "y")
     if ws is None:
         need = spw_spmv_ep_workspace_bytes(h, B)
         ws = torch.zeros(need, dtype=torch.uint8, device=x.device) if need else None
+    pws, nws = (None, 0) if ws is None else (ws.data_ptr(), _nbytes(ws))
     _check("spw_spmv_ep", lib().spw_spmv_ep(
-        ctypes.byref(h), _ptr(buf), _ptr(x2), B, ldx, float(threshold), _ptr(act_bits),
-        ctypes.byref(ep), _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(h), buf.data_ptr(), x2.data_ptr(), B, ldx, float(threshold), _ptr(act_bits),
+        ctypes.byref(ep), py, ldy, pws, nws, _stream()))
     return y
 
 
@@ -893,24 +907,24 @@ def spw_spmm_ep_workspace_bytes(hdr, M: int) -> int:
     return int(lib().spw_spmm_ep_workspace_bytes(ctypes.byref(_hdr(hdr)), int(M)))
 
 
+@_on_stream
 def spw_spmm_ep(hdr, buf: torch.Tensor, X: torch.Tensor, bias: torch.Tensor | None = None,
                 act=SPW_ACT_NONE, residual: torch.Tensor | None = None,
-                Y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-                stream=None) -> torch.Tensor:
+                Y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Prefill with an epilogue: Y = act(X . W_masked^T + bias) + residual (M x N fp16).
 
     bias, act and residual as spw_spmv_ep.  ws: spw_spmm_ep_workspace_bytes(hdr, M) bytes of
     any content (allocated here when not given)."""
     h = _hdr(hdr)
-    X2, M, ldx = _x_of(X, h.K, "X")
+    X2, M, ldx = _mat(X, None, h.K, "X")
     _same_device(X, buf, bias, residual, Y, ws)
     ep = _epilogue(bias, act, residual, M, h.N)
     _need_buf(buf, h)
-    Y, Y2, ldy = _out(Y, M, h.N, X, "Y")
-    ws = _ws_of(ws, spw_spmm_ep_workspace_bytes(h, M), X)
+    Y, pY, ldy = _out(Y, M, h.N, X, "Y")
+    ws, pws, nws = _ws_of(ws, spw_spmm_ep_workspace_bytes(h, M), X)
     _check("spw_spmm_ep", lib().spw_spmm_ep(
-        ctypes.byref(h), _ptr(buf), _ptr(X2), M, ldx, ctypes.byref(ep), _ptr(Y2), ldy, _ptr(ws),
-        _nbytes(ws), _stream(stream)))
+        ctypes.byref(h), buf.data_ptr(), X2.data_ptr(), M, ldx, ctypes.byref(ep), pY, ldy, pws, nws,
+        _stream()))
     return Y
 
 
@@ -919,32 +933,33 @@ def spw_spmm_ffn_workspace_bytes(hdr_gate, hdr_up, M: int) -> int:
                                                   ctypes.byref(_hdr(hdr_up)), int(M)))
 
 
+@_on_stream
 def spw_spmm_ffn(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor, X: torch.Tensor,
                  act=SPW_ACT_SILU, save: bool = False, H: torch.Tensor | None = None,
                  G: torch.Tensor | None = None, U: torch.Tensor | None = None,
-                 ws: torch.Tensor | None = None, stream=None):
+                 ws: torch.Tensor | None = None):
     """Prefill of the gated block in one kernel: H = act(X . W_gate^T) * (X . W_up^T), M x N.
 
     Returns H, or (H, G, U) with the two projections when save is set or G and U are given
     (what spw_spmm_ffn_backward takes).  ws: spw_spmm_ffn_workspace_bytes(...) bytes."""
     hg, hu = _hdr(hdr_gate), _hdr(hdr_up)
-    X2, M, ldx = _x_of(X, hg.K, "X")
+    X2, M, ldx = _mat(X, None, hg.K, "X")
     if (G is None) != (U is None):
         raise ValueError("G and U go together")
     save = save or G is not None
     _same_device(X, buf_gate, buf_up, H, G, U, ws)
     _need_buf(buf_gate, hg, "buf_gate")
     _need_buf(buf_up, hu, "buf_up")
-    H, H2, ldh = _out(H, M, hg.N, X, "H")
-    G2 = U2 = None
+    H, pH, ldh = _out(H, M, hg.N, X, "H")
+    pG = pU = None
     ldg = ldu = 0
     if save:
-        G, G2, ldg = _out(G, M, hg.N, X, "G")
-        U, U2, ldu = _out(U, M, hg.N, X, "U")
-    ws = _ws_of(ws, spw_spmm_ffn_workspace_bytes(hg, hu, M), X)
+        G, pG, ldg = _out(G, M, hg.N, X, "G")
+        U, pU, ldu = _out(U, M, hg.N, X, "U")
+    ws, pws, nws = _ws_of(ws, spw_spmm_ffn_workspace_bytes(hg, hu, M), X)
     _check("spw_spmm_ffn", lib().spw_spmm_ffn(
-        ctypes.byref(hg), _ptr(buf_gate), ctypes.byref(hu), _ptr(buf_up), _ptr(X2), M, ldx, _act(act),
-        _ptr(H2), ldh, _ptr(G2), ldg, _ptr(U2), ldu, _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(hg), buf_gate.data_ptr(), ctypes.byref(hu), buf_up.data_ptr(), X2.data_ptr(), M, ldx, _act(act),
+        pH, ldh, pG, ldg, pU, ldu, pws, nws, _stream()))
     return (H, G, U) if save else H
 
 
@@ -953,41 +968,42 @@ def spw_spmm_ffn_backward_workspace_bytes(hdr_gate, hdr_up, M: int) -> int:
         ctypes.byref(_hdr(hdr_gate)), ctypes.byref(_hdr(hdr_up)), int(M)))
 
 
+@_on_stream
 def spw_spmm_ffn_backward(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor,
                           X: torch.Tensor | None, G: torch.Tensor, U: torch.Tensor, dH: torch.Tensor,
                           act=SPW_ACT_SILU, need_dx: bool = True, need_dv: bool = True,
                           dX: torch.Tensor | None = None, dV_gate: torch.Tensor | None = None,
-                          dV_up: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-                          stream=None):
+                          dV_up: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """Gradients of spw_spmm_ffn, the patterns held fixed: (dX, dV_gate, dV_up).
 
     dV_*: the kept weights' gradients in the order of the buffers' values sections (1-D fp16).
     need_dx / need_dv False leaves that part out (None in its place; X may then be None for
     need_dv False).  ws: spw_spmm_ffn_backward_workspace_bytes(...) bytes."""
     hg, hu = _hdr(hdr_gate), _hdr(hdr_up)
-    G2, ldg = _rows(_half(G, "G"), "G")
-    M = G2.shape[0]
-    _in(G, M, hg.N, "G")
-    U2, ldu = _in(U, M, hg.N, "U")
-    dH2, lddh = _in(dH, M, hg.N, "dH")
+    G2, M, ldg = _mat(G, None, hg.N, "G")
+    U2, _, ldu = _mat(U, M, hg.N, "U")
+    dH2, _, lddh = _mat(dH, M, hg.N, "dH")
     if need_dv and X is None:
         raise ValueError("the weights' gradients need X")
-    X2, ldx = _in(X, M, hg.K, "X") if X is not None else (None, 0)
+    pX, ldx = None, 0
+    if X is not None:
+        X2, _, ldx = _mat(X, M, hg.K, "X")
+        pX = X2.data_ptr()
     _same_device(G, U, dH, X, buf_gate, buf_up, dX, dV_gate, dV_up, ws)
     _need_buf(buf_gate, hg, "buf_gate")
     _need_buf(buf_up, hu, "buf_up")
-    dX2, lddx = None, 0
+    pdX, lddx = None, 0
     if need_dx:
-        dX, dX2, lddx = _out(dX, M, hg.K, G, "dX")
+        dX, pdX, lddx = _out(dX, M, hg.K, G, "dX")
     else:
         dX = None
-    dV_gate = _packed(dV_gate, hg, G, "dV_gate") if need_dv else None
-    dV_up = _packed(dV_up, hu, G, "dV_up") if need_dv else None
-    ws = _ws_of(ws, spw_spmm_ffn_backward_workspace_bytes(hg, hu, M), G)
+    dV_gate, pVg = _packed(dV_gate, hg, buf_gate, "dV_gate") if need_dv else (None, None)
+    dV_up, pVu = _packed(dV_up, hu, buf_up, "dV_up") if need_dv else (None, None)
+    ws, pws, nws = _ws_of(ws, spw_spmm_ffn_backward_workspace_bytes(hg, hu, M), G)
     _check("spw_spmm_ffn_backward", lib().spw_spmm_ffn_backward(
-        ctypes.byref(hg), _ptr(buf_gate), ctypes.byref(hu), _ptr(buf_up), _ptr(X2), M, ldx, _act(act),
-        _ptr(G2), ldg, _ptr(U2), ldu, _ptr(dH2), lddh, _ptr(dX2), lddx, _packed_ptr(dV_gate, buf_gate),
-        _packed_ptr(dV_up, buf_up), _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(hg), buf_gate.data_ptr(), ctypes.byref(hu), buf_up.data_ptr(), pX, M, ldx, _act(act),
+        G2.data_ptr(), ldg, U2.data_ptr(), ldu, dH2.data_ptr(), lddh, pdX, lddx, pVg,
+        pVu, pws, nws, _stream()))
     return dX, dV_gate, dV_up
 
 
@@ -995,28 +1011,32 @@ def spw_spmm_backward_workspace_bytes(hdr, M: int) -> int:
     return int(lib().spw_spmm_backward_workspace_bytes(ctypes.byref(_hdr(hdr)), int(M)))
 
 
+@_on_stream
 def spw_spmm_backward(hdr, buf: torch.Tensor, X: torch.Tensor | None, dY: torch.Tensor,
                       need_dx: bool = True, need_dv: bool = True, dX: torch.Tensor | None = None,
-                      dV: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+                      dV: torch.Tensor | None = None, ws: torch.Tensor | None = None):
     """Gradients of Y = X . W_masked^T, the pattern held fixed: (dX, dV); dV, need_* and X as
     spw_spmm_ffn_backward.  ws: spw_spmm_backward_workspace_bytes(hdr, M) bytes."""
     h = _hdr(hdr)
-    dY2, M, lddy = _x_of(dY, h.N, "dY")
+    dY2, M, lddy = _mat(dY, None, h.N, "dY")
     if need_dv and X is None:
         raise ValueError("the weight's gradient needs X")
-    X2, ldx = _in(X, M, h.K, "X") if X is not None else (None, 0)
+    pX, ldx = None, 0
+    if X is not None:
+        X2, _, ldx = _mat(X, M, h.K, "X")
+        pX = X2.data_ptr()
     _same_device(dY, X, buf, dX, dV, ws)
     _need_buf(buf, h)
-    dX2, lddx = None, 0
+    pdX, lddx = None, 0
     if need_dx:
-        dX, dX2, lddx = _out(dX, M, h.K, dY, "dX")
+        dX, pdX, lddx = _out(dX, M, h.K, dY, "dX")
     else:
         dX = None
-    dV = _packed(dV, h, dY, "dV") if need_dv else None
-    ws = _ws_of(ws, spw_spmm_backward_workspace_bytes(h, M), dY)
+    dV, pV = _packed(dV, h, buf, "dV") if need_dv else (None, None)
+    ws, pws, nws = _ws_of(ws, spw_spmm_backward_workspace_bytes(h, M), dY)
     _check("spw_spmm_backward", lib().spw_spmm_backward(
-        ctypes.byref(h), _ptr(buf), _ptr(X2), M, ldx, _ptr(dY2), lddy, _ptr(dX2), lddx,
-        _packed_ptr(dV, buf), _ptr(ws), _nbytes(ws), _stream(stream)))
+        ctypes.byref(h), buf.data_ptr(), pX, M, ldx, dY2.data_ptr(), lddy, pdX, lddx,
+        pV, pws, nws, _stream()))
     return dX, dV
 
 
@@ -1076,10 +1096,10 @@ class SparseLinear:
             need = spw_spmv_ep_workspace_bytes(self.hdr, B)
             self._ws[("ep", B)] = torch.zeros(need, dtype=torch.uint8, device=self.buf.device) if need else None
         return spw_spmv_ep(self.hdr, self.buf, x2, threshold, act_bits, bias, act, residual, y,
-                           self._ws[("ep", B)], stream)
+                           self._ws[("ep", B)], stream=stream)
 
     def spmm_ep(self, X, bias=None, act=SPW_ACT_NONE, residual=None, Y=None, ws=None, stream=None):
-        return spw_spmm_ep(self.hdr, self.buf, X, bias, act, residual, Y, ws, stream)
+        return spw_spmm_ep(self.hdr, self.buf, X, bias, act, residual, Y, ws, stream=stream)
 
     def spmm_backward(self, X, dY, need_dx=True, need_dv=True, ws=None, stream=None):
         return spw_spmm_backward(self.hdr, self.buf, X, dY, need_dx, need_dv, ws=ws, stream=stream)
@@ -1117,7 +1137,7 @@ class SparseFFN:
 
     def spmm(self, X, save=False, H=None, G=None, U=None, ws=None, stream=None):
         return spw_spmm_ffn(self.gate.hdr, self.gate.buf, self.up.hdr, self.up.buf, X, self.act, save,
-                            H, G, U, ws, stream)
+                            H, G, U, ws, stream=stream)
 
     def backward(self, X, G, U, dH, need_dx=True, need_dv=True, ws=None, stream=None):
         return spw_spmm_ffn_backward(self.gate.hdr, self.gate.buf, self.up.hdr, self.up.buf, X, G, U, dH,

@@ -66,6 +66,8 @@ struct ExpandParams {
     int strips, ktp;    // strips of an output block; blocks of a row of blocks
     uint32_t warp_smem;
     int* status;
+    uint32_t* clear;    // counters of the products that follow, cleared here
+    uint32_t n_clear;
 };
 
 // One warp writes one 64 x 64 tile of the dense weight, in the blocks that the product reads: p.strips
@@ -74,6 +76,8 @@ struct ExpandParams {
 // entry out (4096 x 8192 at 50 %: 105 MB in 20 us, 5.2 TB/s).
 __global__ void __launch_bounds__(32 * kExpandWarps) expand_kernel(const __grid_constant__ ExpandParams p) {
     extern __shared__ __align__(16) unsigned char smem[];
+    pdl_launch_dependents();  // the product may set itself up; it waits for this grid's end
+    for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < p.n_clear; i += gridDim.x * blockDim.x) p.clear[i] = 0u;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned char* mine = smem + (size_t)warp * p.warp_smem;
     unsigned char* rec = mine;
@@ -407,7 +411,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
     };
     const int half_cols = p.BN / 2;
 
+    // Launched while the kernel before it in the same call still runs.  kEp, kFfn, kDx read what
+    // that kernel writes (the expansion; dG and dU stand before it): the producer waits for
+    // its end, then lets the next kernel of the call start.  kDv reads nothing of the kernel
+    // before it (the input's gradient), which waited itself for dG and dU before it let kDv
+    // start; it only must not end before it, see below.
     uint32_t issued = 0;  // producer: stages loaded
+    if (MODE != kDv && threadIdx.x == 0) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
     if (warp == 0) {
         if (lane == 0) {
             const uint32_t full0 = map_to_rank(smem_u32(&full[0]), 0u);
@@ -696,6 +709,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
     __syncwarp();
     __syncthreads();
     cluster_sync_all();
+    if (MODE == kDv && threadIdx.x == 0) pdl_wait();  // the stream's next work follows both
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2u * kAccCols)
@@ -705,13 +719,16 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
 
 // ------------------------------------------------------------------ dG and dU
 // dG = dH U act'(G), dU = dH act(G) (M x ld, ld = N rounded up to 8; the columns past N are
-// not written and not read), 8 columns per thread.  Memory-bound: 10 bytes an entry.  Rounded
+// not written and not read), 8 columns per thread; clears the products' counters as well.  Memory-bound: 10 bytes an entry.  Rounded
 // to fp16 because they are operands of the products that follow; an overflow becomes an
 // infinity there, which a loss scaler looks for.
 __global__ void __launch_bounds__(256)
 gate_grad_kernel(const uint16_t* __restrict__ G, int ldg, const uint16_t* __restrict__ U, int ldu,
                  const uint16_t* __restrict__ dH, int ldh, int M, int N, int act, int vec,
-                 uint16_t* __restrict__ dG, uint16_t* __restrict__ dU, int ld) {
+                 uint16_t* __restrict__ dG, uint16_t* __restrict__ dU, int ld, uint32_t* __restrict__ clear,
+                 uint32_t n_clear) {
+    pdl_launch_dependents();
+    for (uint32_t i = blockIdx.x * blockDim.x + threadIdx.x; i < n_clear; i += gridDim.x * blockDim.x) clear[i] = 0u;
     const int per_row = (N + 7) / 8;
     const long long n = (long long)M * per_row;
     for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (long long)gridDim.x * blockDim.x) {
@@ -862,22 +879,25 @@ void fill_params(const GemmPlan& g, long long ksteps, GemmParams* p) {
     p->status = device_status_ptr();
 }
 
+// early: may start while the kernel before it, of the same call, still runs.
 template <int MODE>
 int launch_gemm(const GemmPlan& g, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
-                const CUtensorMap& b1, const GemmParams& p, int pairs, cudaStream_t s) {
+                const CUtensorMap& b1, const GemmParams& p, int pairs, bool early, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     const long long n = g.n_units < pairs ? g.n_units : pairs;
     cfg.gridDim = dim3((unsigned)(2 * n));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = g.smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = early ? 2 : 1;
     SPW_CUDA_TRY(cudaLaunchKernelEx(&cfg, gemm_kernel<MODE>, a0, a1, b0, b1, p));
     return SPW_OK;
 }
@@ -888,10 +908,13 @@ uint64_t dense_bytes(const spw_format* h) {
     return round_up_u64(h->n_strips, 4) * (uint64_t)ktp_of(h) * 8192;
 }
 
-// Expands one or two weights (dense row stride 64 n_ktiles).
-int expand(int n, const spw_format* const* hdrs, const void* const* bufs, uint16_t* const* outs, int strips, cudaStream_t s) {
+// Expands one or two weights into blocks of `strips` strips, and clears counters.
+int expand(int n, const spw_format* const* hdrs, const void* const* bufs, uint16_t* const* outs, int strips, void* clear,
+           uint64_t clear_bytes, cudaStream_t s) {
     ExpandParams p;
     memset(&p, 0, sizeof(p));
+    p.clear = (uint32_t*)clear;
+    p.n_clear = (uint32_t)(clear_bytes / 4);
     p.strips = strips;
     p.ktp = ktp_of(hdrs[0]);
     uint32_t units = 0;
@@ -932,11 +955,11 @@ uint64_t map_ld(int ld, int rows) { return 2ull * (rows > 1 ? (uint64_t)ld : rou
 
 
 // Workspace sections: the split counters of each product, the expanded weights, dG and dU
-// where there are any, and the fp32 partials (shared by the products, which run in turn).
+// where there are any, and the fp32 partials.
 struct Layout {
     GemmPlan fwd, dx, dv;
     bool fwd_direct, dx_direct;  // by the direct form (spmm_direct.cu): no workspace
-    uint64_t dv_counters, counters, dense, grads, partials, total;  // counters: the bytes to clear
+    uint64_t dv_counters, dv_partials, counters, dense, grads, partials, total;  // counters: the bytes to clear
     int ldn;
 };
 
@@ -986,7 +1009,8 @@ int make_layout(const spw_format* h, const spw_format* h2, int M, int what, Layo
         rc = plan_gemm(h->N, h->K, weights, ((long long)M + 63) / 64, pairs, &L->dv);
         if (rc != SPW_OK) return rc;
         c += L->dv.counter_bytes;
-        if (L->dv.partial_bytes > part) part = L->dv.partial_bytes;
+        L->dv_partials = part;  // beside those of dX: the two may run at the same time
+        part += L->dv.partial_bytes;
     }
     L->counters = c;
     L->dense = c;
@@ -1042,16 +1066,15 @@ int run_forward(const Layout& L, const spw_format* const* hdrs, const void* cons
     p.ktp = ktp_of(h);
     p.counters = (uint32_t*)ws;
     p.partials = (float*)(ws + L.partials);
-    if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
-    rc = expand(kWeights, hdrs, bufs, dense, g.BN / 128, s);
+    rc = expand(kWeights, hdrs, bufs, dense, g.BN / 128, ws, L.counters, s);
     if (rc != SPW_OK) return rc;
-    return launch_gemm<MODE>(g, a, a, b[0], b[kWeights - 1], p, gemm_pairs(), s);
+    return launch_gemm<MODE>(g, a, a, b[0], b[kWeights - 1], p, gemm_pairs(), true, s);
 }
 
 // dX = sum over the weights of dY_w W_w, by the form that the layout chose.
 int run_dx(const spw_format* const* hdrs, const void* const* bufs, int weights, const Layout& L, uint8_t* ws,
            uint32_t* counters, const uint16_t* const* dY, const uint64_t* ld_bytes, int M, uint16_t* dX, int lddx,
-           cudaStream_t s) {
+           bool early, cudaStream_t s) {
     const GemmPlan& g = L.dx;
     const spw_format* h = hdrs[0];
     PrefillOut o;
@@ -1073,11 +1096,12 @@ int run_dx(const spw_format* const* hdrs, const void* const* bufs, int weights, 
         }
         c.M = M;
         c.out = o;
+        c.early = early;
         return direct_launch(c, s);
     }
     uint16_t* dense[2];
     for (int w = 0; w < weights; w++) dense[w] = (uint16_t*)(ws + L.dense + (uint64_t)w * dense_bytes(h));
-    const int erc = expand(weights, hdrs, bufs, dense, 1, s);
+    const int erc = expand(weights, hdrs, bufs, dense, 1, nullptr, 0, s);
     if (erc != SPW_OK) return erc;
     CUtensorMap a[2], b[2];
     for (int w = 0; w < weights; w++) {
@@ -1099,13 +1123,13 @@ int run_dx(const spw_format* const* hdrs, const void* const* bufs, int weights, 
     p.o = o;
     p.counters = counters;
     p.partials = (float*)(ws + L.partials);
-    return launch_gemm<kDx>(g, a[0], a[1], b[0], b[1], p, gemm_pairs(), s);
+    return launch_gemm<kDx>(g, a[0], a[1], b[0], b[1], p, gemm_pairs(), true, s);
 }
 
 // Gradients of the kept weights, dY_w^T X at their positions, packed as the values are.
 int run_dv(const spw_format* const* hdrs, const void* const* bufs, int weights, const Layout& L, uint8_t* ws,
            uint32_t* counters, const uint16_t* const* dY, const uint64_t* ld_bytes, const uint16_t* X, int ldx, int M,
-           uint16_t* const* dV, cudaStream_t s) {
+           uint16_t* const* dV, bool early, cudaStream_t s) {
     const GemmPlan& g = L.dv;
     const spw_format* h = hdrs[0];
     CUtensorMap a[2], b;
@@ -1129,8 +1153,8 @@ int run_dv(const spw_format* const* hdrs, const void* const* bufs, int weights, 
     p.o.rows = (int)h->N;
     p.o.cols = (int)h->K;
     p.counters = counters;
-    p.partials = (float*)(ws + L.partials);
-    return launch_gemm<kDv>(g, a[0], a[1], b, b, p, gemm_pairs(), s);
+    p.partials = (float*)(ws + L.partials + L.dv_partials);
+    return launch_gemm<kDv>(g, a[0], a[1], b, b, p, gemm_pairs(), early, s);
 }
 
 }  // namespace
@@ -1287,8 +1311,8 @@ int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate, co
     if (most <= 0) return SPW_ERR_CUDA;
     const long long grid = (n + 255) / 256 < most ? (n + 255) / 256 : most;
     const int vec = ldg % 8 == 0 && ldu % 8 == 0 && lddh % 8 == 0 ? 1 : 0;
-    if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
-    gate_grad_kernel<<<(unsigned)grid, 256, 0, s>>>(d_G, ldg, d_U, ldu, d_dH, lddh, M, N, act, vec, dG, dU, L.ldn);
+    gate_grad_kernel<<<(unsigned)grid, 256, 0, s>>>(d_G, ldg, d_U, ldu, d_dH, lddh, M, N, act, vec, dG, dU, L.ldn,
+                                                    (uint32_t*)ws, (uint32_t)(L.counters / 4));
     SPW_LAUNCH_CHECK();
     const spw_format* hdrs[2] = {hdr_gate, hdr_up};
     const void* bufs[2] = {d_buf_gate, d_buf_up};
@@ -1296,12 +1320,12 @@ int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate, co
     const uint64_t ld_bytes[2] = {2ull * L.ldn, 2ull * L.ldn};
     uint32_t* counters = (uint32_t*)ws;
     if (d_dX) {
-        rc = run_dx(hdrs, bufs, 2, L, ws, counters, dY, ld_bytes, M, d_dX, lddx, s);
+        rc = run_dx(hdrs, bufs, 2, L, ws, counters, dY, ld_bytes, M, d_dX, lddx, true, s);
         if (rc != SPW_OK) return rc;
     }
     if (d_dV_gate) {
         uint16_t* dV[2] = {d_dV_gate, d_dV_up};
-        rc = run_dv(hdrs, bufs, 2, L, ws, counters + L.dv_counters / 4, dY, ld_bytes, d_X, ldx, M, dV, s);
+        rc = run_dv(hdrs, bufs, 2, L, ws, counters + L.dv_counters / 4, dY, ld_bytes, d_X, ldx, M, dV, d_dX != nullptr, s);
     }
     return rc;
 }
@@ -1338,11 +1362,11 @@ int spw_spmm_backward(const spw_format* hdr, const void* d_buf, const uint16_t* 
     const uint64_t ld_bytes[1] = {map_ld(lddy, M)};
     if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
     if (d_dX) {
-        rc = run_dx(&hdr, &d_buf, 1, L, ws, counters, &d_dY, ld_bytes, M, d_dX, lddx, s);
+        rc = run_dx(&hdr, &d_buf, 1, L, ws, counters, &d_dY, ld_bytes, M, d_dX, lddx, false, s);
         if (rc != SPW_OK) return rc;
     }
     if (d_dV)
-        rc = run_dv(&hdr, &d_buf, 1, L, ws, counters + L.dv_counters / 4, &d_dY, ld_bytes, d_X, ldx, M, &d_dV, s);
+        rc = run_dv(&hdr, &d_buf, 1, L, ws, counters + L.dv_counters / 4, &d_dY, ld_bytes, d_X, ldx, M, &d_dV, d_dX != nullptr, s);
     return rc;
 }
 

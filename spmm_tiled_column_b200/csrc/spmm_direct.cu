@@ -209,8 +209,14 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
     const uint32_t tmem = *tmem_slot;
     const int tok = p.MT / p.nh;  // tokens of an MMA
 
+    // kDx may have been launched while the kernel that writes dG and dU still runs: warp 0, which
+    // alone reads them, waits for its end, then lets the next kernel of the call start.
     int x_issued = 0, r_issued = 0;
     if (warp == 0) {
+        if constexpr (MODE == kDx) {
+            pdl_wait();
+            pdl_launch_dependents();
+        }
         if constexpr (MODE == kDecode) {
             // Rows with the rule applied, written where TMA would put them (128-byte swizzle).  A
             // lane has four 16-byte chunks of the 16 x 64 tile: rows lane / 8 + 4 i, columns 8 c ..
@@ -773,13 +779,15 @@ int direct_launch(const DirectCall& c, cudaStream_t s) {
     cfg.blockDim = dim3((unsigned)threads_of(g.groups));
     cfg.dynamicSmemBytes = g.smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)g.parts;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = c.early ? 2 : 1;
     void* args[3] = {&tx[0], &tx[1], &p};
     SPW_CUDA_TRY(cudaLaunchKernelExC(&cfg, kernel_for(c.mode, g.groups), args));
     return SPW_OK;

@@ -39,6 +39,7 @@ struct DirectCall {
     int ldx;
     float t;
     const uint32_t* act_bits;
+    bool early;  // may start while the kernel before it, of the same call, still runs
 };
 
 // Estimated time in microseconds (< 0: the form cannot run this product), and the launch.
