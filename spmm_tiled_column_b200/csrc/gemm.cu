@@ -132,6 +132,7 @@ constexpr int kCtaRows = 128;  // accumulator rows per CTA; 256 per pair
 constexpr int kBK = 64;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kStageBlocks = 2;  // blocks of 64 along the reduction in a stage
 constexpr int kMaxStages = 8;
 constexpr uint32_t kABytes = kCtaRows * kBK * 2;  // 16 KB
 constexpr int kAccCols = 256;                     // columns between the two accumulators
@@ -142,7 +143,7 @@ struct GemmParams {
     int n_units, n_whole, parts;
     int ksteps, kseg;  // reduction blocks of 64 of a tile; those of its first segment (kDx)
     int BN, stages;
-    uint32_t block_bytes, stage_bytes, off_bar;  // this CTA's operands, 64 deep; two of them
+    uint32_t block_bytes, stage_bytes, off_bar;  // this CTA's operands, 64 deep; kStageBlocks of them
     uint32_t off_stage;  // the epilogue warps' blocks
     long long wait_limit;
     int* status;
@@ -190,12 +191,13 @@ __device__ inline Unit unit_of(const GemmParams& p, int u) {
     return w;
 }
 
-// Blocks of 64 along the reduction that the stage starting at block k holds: two, or one at
-// the end of the unit's range or (kDx) of a segment.  A stage of two halves the barrier
-// traffic for each MMA: 64-deep stages ran 0.39 us a block of 64 against 0.32.
+// Blocks of 64 along the reduction that the stage starting at block k holds: fewer at the end
+// of the unit's range or (kDx) of a segment.
 template <int MODE>
 __device__ inline int blocks_at(const GemmParams& p, int k, int k1) {
-    return k + 1 < k1 && (MODE != kDx || k + 1 != p.kseg) ? 2 : 1;
+    int n = min(kStageBlocks, k1 - k);
+    if (MODE == kDx && k < p.kseg) n = min(n, p.kseg - k);
+    return n;
 }
 
 // The same barrier in both CTAs of the pair, once the MMAs issued so far have completed.
@@ -446,7 +448,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                     const CUtensorMap* mb = (MODE == kFfn ? rank != 0 : MODE == kDx && second) ? &tb1 : &tb0;
                     for (int i = 0; i < n; i++) {
                         const uint32_t a = sbase + (uint32_t)s * p.stage_bytes + (uint32_t)i * kABytes;
-                        const uint32_t b = sbase + (uint32_t)s * p.stage_bytes + 2 * kABytes + (uint32_t)(i * half_cols * 128);
+                        const uint32_t b = sbase + (uint32_t)s * p.stage_bytes + kStageBlocks * kABytes + (uint32_t)(i * half_cols * 128);
                         const int kc = kBK * (MODE == kDx && second ? k + i - p.kseg : k + i);
                         if constexpr (A_MN) {
                             tma_load_2d_pair(a, ma, arow, kc, bar);
@@ -472,7 +474,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
     } else if (warp == 1 && rank == 0) {
         // ------------------------------------------------------------ MMAs
         const uint32_t idesc = idesc_f16(2 * kCtaRows, p.BN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-        const uint32_t b0 = sbase + 2 * kABytes;
+        const uint32_t b0 = sbase + kStageBlocks * kABytes;
         const uint64_t ad0 = A_MN ? umma_desc_mn_sw128(sbase) : umma_desc_sw128(sbase);
         const uint64_t bd0 = MODE == kDv   ? umma_desc_mn_sw128(b0)
                              : MODE == kDx ? umma_desc_plain(b0, 128, 1024)
@@ -848,7 +850,7 @@ int plan_gemm(long long rows, long long cols, int problems, long long ksteps, in
     g->counter_bytes = round_up_u64(8ull * (uint64_t)split, 256);
     g->partial_bytes = 4ull * (uint64_t)split * g->parts * 2 * g->BN * kCtaRows;
     g->block_bytes = kABytes + (uint32_t)g->BN / 2 * 128;
-    g->stage_bytes = 2 * g->block_bytes;
+    g->stage_bytes = kStageBlocks * g->block_bytes;
     const uint32_t bars = 8u * (2 * kMaxStages + 5) + 32u;
     const uint32_t blocks = 4u * kEpiWarps * 32 * 33;
     g->stages = (int)((kSmemLimit - 1024 - bars - blocks) / g->stage_bytes);
