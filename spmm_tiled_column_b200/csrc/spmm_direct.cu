@@ -352,21 +352,24 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
             const uint32_t dst = sbase + p.off_raw + (uint32_t)slot * p.raw_bytes;
             pointers(base + 16);
             bool ok = true;
-            for (int j = 0; j < 16 && base + j < nk && ok; j++) {
-                if (lane >> 1 == j) {
-                    ok = last < 0 || wait_or_abort(smem_u32(&r_empty[last % kRing]), (uint32_t)(last / kRing) & 1u, abort_flag,
-                                                   p.wait_limit);
-                    if (ok) {
-                        r_info[2 * (n % kRing) + q] = fits ? vbytes >> 4 : 0xFFFFFFFFu;
-                        mbar_arrive_expect_tx(bar, fits ? 512u + vbytes : 0u);
-                        if (fits) bulk_g2s(dst + 512u * q, bits, 512u, bar);
-                        if (vbytes) bulk_g2s(dst + 1024u + p.val_slot * q, vals, vbytes, bar);
-                    } else {
-                        flag_abort(abort_flag, p.status);
-                    }
+            for (int j = 0; j < 16 && base + j < nk; j++) {
+                // both lanes of a step issue, or none: what is in flight is then known
+                const bool turn = lane >> 1 == j;
+                ok = __all_sync(0xffffffffu, !turn || last < 0 ||
+                                                 wait_or_abort(smem_u32(&r_empty[last % kRing]), (uint32_t)(last / kRing) & 1u,
+                                                               abort_flag, p.wait_limit));
+                if (!ok) {
+                    if (lane == 0) flag_abort(abort_flag, p.status);
+                    break;
                 }
-                ok = __all_sync(0xffffffffu, ok);
-                if (ok) r_issued++;
+                if (turn) {
+                    r_info[2 * (n % kRing) + q] = fits ? vbytes >> 4 : 0xFFFFFFFFu;
+                    mbar_arrive_expect_tx(bar, fits ? 512u + vbytes : 0u);
+                    if (fits) bulk_g2s(dst + 512u * q, bits, 512u, bar);
+                    if (vbytes) bulk_g2s(dst + 1024u + p.val_slot * q, vals, vbytes, bar);
+                }
+                __syncwarp();
+                r_issued++;
             }
             if (!ok) break;
             slot += 16;
