@@ -121,7 +121,6 @@ struct SpmvParams {
     const uint16_t* bias;
     const uint16_t* residual;
     int ldr, act;
-    int ep;  // nonzero: apply it
 };
 
 __host__ __device__ constexpr int xt_stride(int B) {
@@ -485,17 +484,16 @@ __device__ void ffn_strip(const SpmvParams& p, int s, int lane) {
     }
 }
 
-// The result for row r of batch row b: the sum, or the epilogue on it (rows below N only;
-// kept out of line, so that the decode loop's registers do not pay for it).
-__device__ __noinline__ float epilogue_value(const SpmvParams& p, int b, int r, float v) {
-    if (p.bias) v += __half2float(__ushort_as_half(p.bias[r]));
-    v = act_f32(v, p.act);
-    if (p.residual) v += __half2float(__ushort_as_half(p.residual[(size_t)b * p.ldr + r]));
-    return v;
-}
+// The result for row r of batch row b: the sum, or the epilogue on it.  (A kernel of its own:
+// a test of p at run time cost the plain decode step of the 7B layer 1.5 %.)
+template <bool EP>
 __device__ inline void store_result(const SpmvParams& p, const SpmvLayer& L, int b, int r, float v) {
     if (r >= L.N) return;
-    if (p.ep) v = epilogue_value(p, b, r, v);
+    if constexpr (EP) {
+        if (p.bias) v += __half2float(__ushort_as_half(p.bias[r]));
+        v = act_f32(v, p.act);
+        if (p.residual) v += __half2float(__ushort_as_half(p.residual[(size_t)b * p.ldr + r]));
+    }
     L.y[(size_t)b * L.ldy + r] = __half_as_ushort(__float2half_rn(v));
 }
 
@@ -504,7 +502,7 @@ __device__ inline void store_result(const SpmvParams& p, const SpmvLayer& L, int
 // strip held by one warp) or publish the fp32 partials and let the strip's last
 // contributor sum every piece in a fixed order (deterministic), then run the FFN step;
 // the accumulators restart at zero.
-template <int B>
+template <int B, bool EP>
 __device__ inline void finish_piece(const SpmvParams& p, const SpmvLayer& L, const Cursor& cur, int i,
                                     int ntiles, int gw, int lane, float* acc0, float* acc1) {
     const int T = p.n_tiles, PW = p.total_warps;
@@ -520,8 +518,8 @@ __device__ inline void finish_piece(const SpmvParams& p, const SpmvLayer& L, con
     if (count == 1) {
 #pragma unroll
         for (int b = 0; b < B; b++) {
-            store_result(p, L, b, r0, acc0[b]);
-            store_result(p, L, b, r0 + 1, acc1[b]);
+            store_result<EP>(p, L, b, r0, acc0[b]);
+            store_result<EP>(p, L, b, r0 + 1, acc1[b]);
         }
         finished = true;
     } else {
@@ -567,10 +565,10 @@ __device__ inline void finish_piece(const SpmvParams& p, const SpmvLayer& L, con
                 acc.w += __shfl_xor_sync(0xffffffffu, acc.w, 16);
                 const int r = s * kStripRows + r4;
                 if (half == 0) {
-                    store_result(p, L, b, r, acc.x);
-                    store_result(p, L, b, r + 1, acc.y);
-                    store_result(p, L, b, r + 2, acc.z);
-                    store_result(p, L, b, r + 3, acc.w);
+                    store_result<EP>(p, L, b, r, acc.x);
+                    store_result<EP>(p, L, b, r + 1, acc.y);
+                    store_result<EP>(p, L, b, r + 2, acc.z);
+                    store_result<EP>(p, L, b, r + 3, acc.w);
                 }
             }
             if (lane == 0) L.counters[s] = 0u;
@@ -583,7 +581,7 @@ __device__ inline void finish_piece(const SpmvParams& p, const SpmvLayer& L, con
 }
 
 // Consumer warp gw: its tile range, decoded from its ring; partial sums flushed per strip.
-template <int B>
+template <int B, bool EP>
 __device__ void consume(const SpmvParams& p, unsigned char* reg, int gw, int lane) {
     constexpr int XS = xt_stride(B);
     constexpr int PG = pair_group(B);
@@ -740,7 +738,7 @@ __device__ void consume(const SpmvParams& p, unsigned char* reg, int gw, int lan
             phase ^= 1u;
         }
 
-        finish_piece<B>(p, L, cur, i, ntiles, gw, lane, acc0, acc1);
+        finish_piece<B, EP>(p, L, cur, i, ntiles, gw, lane, acc0, acc1);
     }
 }
 
@@ -872,7 +870,7 @@ __device__ inline int sp_prepare(const SpmvParams& p, unsigned char* reg, uint32
     return n_act;
 }
 
-template <int B>
+template <int B, bool EP>
 __device__ void consume_sparse(const SpmvParams& p, unsigned char* reg, int gw, int lane) {
     constexpr int XS = xt_stride(B);
     constexpr int PG = pair_group(B);
@@ -939,7 +937,7 @@ __device__ void consume_sparse(const SpmvParams& p, unsigned char* reg, int gw, 
         }
         pin_acc<B>(acc0, acc1);
         __syncwarp();
-        finish_piece<B>(p, p.L[cur.l], cur, i, ntiles, gw, lane, acc0, acc1);
+        finish_piece<B, EP>(p, p.L[cur.l], cur, i, ntiles, gw, lane, acc0, acc1);
         cur = d1.c;
         n_cur = n_next;
         all_cur = all_next;
@@ -947,7 +945,7 @@ __device__ void consume_sparse(const SpmvParams& p, unsigned char* reg, int gw, 
     }
 }
 
-template <int B>
+template <int B, bool EP>
 __global__ void __launch_bounds__((kMaxConsumers + 1) * 32, B <= 8 ? 2 : 1)
 spmv_kernel(const __grid_constant__ SpmvParams p) {
     extern __shared__ __align__(1024) unsigned char smem[];
@@ -971,9 +969,9 @@ spmv_kernel(const __grid_constant__ SpmvParams p) {
         return;
     }
     if (p.sparse_fetch)
-        consume_sparse<B>(p, regions + (size_t)warp * p.warp_smem, blockIdx.x * W + warp, lane);
+        consume_sparse<B, EP>(p, regions + (size_t)warp * p.warp_smem, blockIdx.x * W + warp, lane);
     else
-        consume<B>(p, regions + (size_t)warp * p.warp_smem, blockIdx.x * W + warp, lane);
+        consume<B, EP>(p, regions + (size_t)warp * p.warp_smem, blockIdx.x * W + warp, lane);
 }
 
 struct Plan {
@@ -1075,18 +1073,18 @@ int make_plan(int n, const spw_format* h, int B, Plan* pl, bool want_sparse = fa
     return SPW_OK;
 }
 
-template <int B>
+template <int B, bool EP>
 int launch(const Plan& pl, const SpmvParams& prm, cudaStream_t s) {
     static size_t attr_smem[kMaxDevices];
     int dev = 0;
     SPW_CUDA_TRY(cudaGetDevice(&dev));
     if (dev < 0 || dev >= kMaxDevices) return SPW_ERR_CUDA;
     if (attr_smem[dev] < pl.smem) {
-        SPW_CUDA_TRY(cudaFuncSetAttribute(spmv_kernel<B>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        SPW_CUDA_TRY(cudaFuncSetAttribute((spmv_kernel<B, EP>), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                           (int)pl.smem));
         // The grid is sized for this many CTAs per SM; ask for the full shared-memory
         // carveout so small per-CTA footprints do not lower the residency.
-        SPW_CUDA_TRY(cudaFuncSetAttribute(spmv_kernel<B>,
+        SPW_CUDA_TRY(cudaFuncSetAttribute((spmv_kernel<B, EP>),
                                           cudaFuncAttributePreferredSharedMemoryCarveout,
                                           (int)cudaSharedmemCarveoutMaxShared));
         attr_smem[dev] = pl.smem;
@@ -1101,7 +1099,7 @@ int launch(const Plan& pl, const SpmvParams& prm, cudaStream_t s) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = launch_overlap() ? 1 : 0;
-    SPW_CUDA_TRY(cudaLaunchKernelEx(&cfg, spmv_kernel<B>, prm));
+    SPW_CUDA_TRY(cudaLaunchKernelEx(&cfg, spmv_kernel<B, EP>, prm));
     SPW_LAUNCH_CHECK();
     return SPW_OK;
 }
@@ -1191,16 +1189,16 @@ int decode_group_launch(int n, const spw_format* hdrs, const void* const* bufs,
         prm.ffn_pairs = ffn->pairs;
         prm.ffn_t = ffn->t;
     }
-    if (ep && (ep->bias || ep->residual || ep->act != SPW_ACT_NONE)) {
+    const bool ep_on = ep && (ep->bias || ep->residual || ep->act != SPW_ACT_NONE);
+    if (ep_on) {
         prm.bias = ep->bias;
         prm.residual = ep->residual;
         prm.ldr = ep->ldr;
         prm.act = ep->act;
-        prm.ep = 1;
     }
     switch (B) {
 #define SPW_CASE(b) \
-    case b: return launch<b>(pl, prm, s);
+    case b: return ep_on ? launch<b, true>(pl, prm, s) : launch<b, false>(pl, prm, s);
         SPW_CASE(1) SPW_CASE(2) SPW_CASE(3) SPW_CASE(4) SPW_CASE(5) SPW_CASE(6) SPW_CASE(7)
         SPW_CASE(8) SPW_CASE(9) SPW_CASE(10) SPW_CASE(11) SPW_CASE(12) SPW_CASE(13)
         SPW_CASE(14) SPW_CASE(15) SPW_CASE(16)
