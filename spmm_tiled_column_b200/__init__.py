@@ -819,7 +819,7 @@ def _mat(t: torch.Tensor, rows: int | None, cols: int, name: str) -> tuple[torch
 def _out(t: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, name: str):
     """An fp16 output of at least rows x cols (allocated when not given): (tensor, address, ld)."""
     if t is None:
-        t = like.new_empty((rows, cols), dtype=torch.float16)
+        t = torch.empty_strided((rows, cols), (cols, 1), dtype=torch.float16, device=like.device)
         return t, t.data_ptr(), cols
     v, ld = _rows(_half(t, name), name)
     _need(v, rows, cols, name)
@@ -836,7 +836,7 @@ def _packed(t: torch.Tensor | None, h, buf: torch.Tensor, name: str) -> tuple[to
     weight's buffer stands for it; nothing is written there.)"""
     n = _values_len(h)
     if t is None:
-        t = buf.new_empty((n,), dtype=torch.float16)
+        t = torch.empty_strided((n,), (1,), dtype=torch.float16, device=buf.device)
     else:
         t = _half(t, name)
         if t.dim() != 1 or (t.numel() > 1 and t.stride(0) != 1) or t.numel() < n:
@@ -849,7 +849,7 @@ def _ws_of(ws: torch.Tensor | None, need: int, like: torch.Tensor):
     if ws is None:
         if not need:
             return None, None, 0
-        ws = like.new_empty((need,), dtype=torch.uint8)
+        ws = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=like.device)
         return ws, ws.data_ptr(), need
     return ws, ws.data_ptr(), _nbytes(ws)
 

@@ -587,8 +587,8 @@ const void* kernel_for(int mode, int groups) {
     }
 }
 
-// CTAs that can be resident at once in clusters of `parts` (the largest shared memory of the
-// variant), per device; 0 when the query fails.
+// CTAs in clusters of `parts` that are resident at one CTA an SM (with the largest shared memory
+// of the variant), per device; 0 when the query fails.
 int resident(int groups, int parts) {
     static int cache[kMaxDevices][2][kMaxParts + 1];
     static std::mutex mu;
@@ -648,16 +648,23 @@ int search_plan(int mode, const spw_format* h, const spw_format* h2, int M, uint
             for (int parts = 1; parts <= kMaxParts && parts <= g.steps; parts++) {
                 const int slots = resident(groups, parts);
                 if (slots <= 0) continue;
-                const double waves = (double)((tiles * parts + slots - 1) / slots);
                 const double steps = (double)((g.steps + parts - 1) / parts);
                 // Measured: a step of two tiles (decoding, and shared memory's share of the tokens);
                 // what a CTA takes before the first and after the last, most of it the exchange of
                 // the pieces.  (4096 x 4096, 4 pieces of 16 steps: 16.4 us at 16 tokens, 19.3 at 128,
-                // 23.5 at 256, 32.8 at 512.)  Two CTAs on an SM slow each other down, but the one
-                // works while the other starts or ends: 11008 x 4096 at 16 tokens 34 us against 39.
-                const double step = groups == 4 ? 0.58 + 0.00056 * g.MT
-                                                : (tiles * parts > device_sm_count() ? 1.2 : 0.8) + 0.0026 * g.MT;
-                const double cost = waves * (steps * step + 6.1 + (parts > 1 ? 0.8 + 0.0235 * g.MT : 0.008 * g.MT));
+                // 23.5 at 256, 32.8 at 512.)  CTAs of two groups go two to an SM, where the one works
+                // while the other starts or ends but both decode more slowly: better where whole
+                // waves fit badly (11008 x 4096 at 16 tokens 34 us against 39, gated 67 against 74;
+                // 4096 x 4096 18.8 against 16.4).
+                const double ends = 6.1 + (parts > 1 ? 0.8 + 0.0235 * g.MT : 0.008 * g.MT);
+                double cost;
+                if (groups == 4) {
+                    cost = (double)((tiles * parts + slots - 1) / slots) * (steps * (0.58 + 0.00056 * g.MT) + ends);
+                } else {
+                    const long long full = tiles * parts / (2 * slots), rest = tiles * parts % (2 * slots);
+                    const double shared = steps * (1.3 + 0.002 * g.MT) + ends, alone = steps * (0.7 + 0.002 * g.MT) + ends;
+                    cost = (double)full * shared + (rest == 0 ? 0.0 : rest <= slots ? alone : shared);
+                }
                 if (best->cost < 0 || cost < best->cost * 0.98) {
                     *best = g;
                     best->parts = parts;
