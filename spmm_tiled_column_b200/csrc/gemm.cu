@@ -598,10 +598,7 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                     load(c, v);
                     if constexpr (MODE == kEp) {
                         if (p.o.bias) add_bias(p.o.bias, col, p.o.cols, v);
-                        if (p.o.act != SPW_ACT_NONE) {
-#pragma unroll
-                            for (int j = 0; j < 32; j++) v[j] = act_f32(v[j], p.o.act);
-                        }
+                        act_all(v, p.o.act);
                     }
                     store_block(stage, lane, p.o.Y, p.o.ldy, MODE == kEp ? p.o.residual : nullptr, p.o.ldr, r0, p.o.rows, col,
                                 p.o.cols, (p.o.vec & 3) == 3, p.o.vec & 16, v);
@@ -619,8 +616,9 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                         store_block(stage, lane, p.o.G, p.o.ldg, nullptr, 0, r0, p.o.rows, col, p.o.cols, p.o.vec & 4, p.o.vec & 32, g);
                         store_block(stage, lane, p.o.U, p.o.ldu, nullptr, 0, r0, p.o.rows, col, p.o.cols, p.o.vec & 8, p.o.vec & 64, v);
                     }
+                    act_all(g, p.o.act);
 #pragma unroll
-                    for (int j = 0; j < 32; j++) v[j] *= act_f32(g[j], p.o.act);
+                    for (int j = 0; j < 32; j++) v[j] *= g[j];
                     store_block(stage, lane, p.o.Y, p.o.ldy, nullptr, 0, r0, p.o.rows, col, p.o.cols, p.o.vec & 1, p.o.vec & 16, v);
                 }
             } else {
@@ -968,12 +966,13 @@ struct Layout {
 constexpr int kForward = 1, kDxOut = 2, kDvOut = 4;
 
 // Whether the direct form takes less time than expansion and product.  Measured: the expansion
-// takes 3.5 us and 0.53 us for a million entries, the product 3 us beside its units, and the
-// clearing of counters 2.  (4096 x 4096: direct / expanded 25 / 29 us at 256 tokens, 36 / 31 at
-// 512; 11008 x 4096: 60 / 62 and 84 / 81.)
+// takes 3.5 us and 0.53 us for a million entries, the product 3 us beside its units and 0.17 for a
+// million entries (what L2 does not keep), and the clearing of counters 2.  (Direct / expanded:
+// 4096 x 4096 with an epilogue 23 / 32 us at 256 tokens, 32 / 33 at 512, 47 / 43 at 1024; gated,
+// 11008 x 4096, 110 / 122 at 256, 137 / 148 at 512, 182 / 168 at 700.)
 bool choose_direct(int mode, const spw_format* h, const spw_format* h2, int M, const GemmPlan& g) {
     const double entries = (h2 ? 2.0 : 1.0) * h->n_strips * (double)h->n_ktiles * kStripRows * kTileCols;
-    const double other = g.cost + 6.5 + entries * 0.53e-6 + (g.counter_bytes ? 2.0 : 0.0);
+    const double other = g.cost + 6.5 + entries * 0.7e-6 + (g.counter_bytes ? 2.0 : 0.0);
     const double direct = direct_cost(mode, h, h2, M);
     return direct >= 0.0 && direct <= other;
 }

@@ -507,8 +507,9 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
                         store4(p.o.G + (size_t)m * p.o.ldg, col, p.o.cols, p.o.vec & 4, v);
                         store4(p.o.U + (size_t)m * p.o.ldu, col, p.o.cols, p.o.vec & 8, u);
                     }
+                    act_all(v, p.o.act);
 #pragma unroll
-                    for (int e = 0; e < 4; e++) v[e] = act_f32(v[e], p.o.act) * u[e];
+                    for (int e = 0; e < 4; e++) v[e] *= u[e];
                     store4(p.o.Y + (size_t)m * p.o.ldy, col, p.o.cols, p.o.vec & 1, v);
                 }
             } else {
@@ -516,8 +517,7 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
                 if (col < p.o.cols) {
                     if constexpr (MODE == kEp || MODE == kDecode) {
                         if (p.o.bias) add4(p.o.bias, col, p.o.cols, true, v);
-#pragma unroll
-                        for (int e = 0; e < 4; e++) v[e] = act_f32(v[e], p.o.act);
+                        act_all(v, p.o.act);
                         if (p.o.residual) add4(p.o.residual + (size_t)m * p.o.ldr, col, p.o.cols, p.o.vec & 2, v);
                     }
                     store4(p.o.Y + (size_t)m * p.o.ldy, col, p.o.cols, p.o.vec & 1, v);
@@ -649,20 +649,23 @@ int search_plan(int mode, const spw_format* h, const spw_format* h2, int M, uint
                 const int slots = resident(groups, parts);
                 if (slots <= 0) continue;
                 const double steps = (double)((g.steps + parts - 1) / parts);
-                // Measured: a step of two tiles (decoding, and shared memory's share of the tokens);
-                // what a CTA takes before the first and after the last, most of it the exchange of
-                // the pieces.  (4096 x 4096, 4 pieces of 16 steps: 16.4 us at 16 tokens, 19.3 at 128,
-                // 23.5 at 256, 32.8 at 512.)  CTAs of two groups go two to an SM, where the one works
-                // while the other starts or ends but both decode more slowly: better where whole
-                // waves fit badly (11008 x 4096 at 16 tokens 34 us against 39, gated 67 against 74;
-                // 4096 x 4096 18.8 against 16.4).
-                const double ends = 6.1 + (parts > 1 ? 0.8 + 0.0235 * g.MT : 0.008 * g.MT);
+                // Fitted to measured times of every split (9 weights, 16 to 400 tokens; the plan it
+                // picks is within 0.1 % of the fastest on average): a step of two tiles (decoding, and
+                // shared memory's share of the tokens; above 256 tokens all SMs' token tiles come near
+                // what L2 delivers), and what a CTA takes before the first and after the last, most of
+                // it the exchange of the pieces.  (4096 x 4096, 4 pieces of 16 steps: 16.2 us at 16
+                // tokens, 19.2 at 128, 23.0 at 256, 32.4 at 512.)  CTAs of two groups go two to an SM,
+                // where the one works while the other starts or ends but both decode more slowly:
+                // better where whole waves fit badly (11008 x 4096 at 16 tokens 34 us against 39, gated
+                // 67 against 74; 4096 x 4096 18.8 against 16.4).
+                const double ends = 5.6 + (parts > 1 ? 0.9 : 0.0) + 0.0235 * g.MT;
                 double cost;
                 if (groups == 4) {
-                    cost = (double)((tiles * parts + slots - 1) / slots) * (steps * (0.58 + 0.00056 * g.MT) + ends);
+                    const double step = 0.55 + 0.0005 * g.MT + (g.MT > 256 ? 0.00055 * (g.MT - 256) : 0.0);
+                    cost = (double)((tiles * parts + slots - 1) / slots) * (steps * step + ends);
                 } else {
                     const long long full = tiles * parts / (2 * slots), rest = tiles * parts % (2 * slots);
-                    const double shared = steps * (1.3 + 0.002 * g.MT) + ends, alone = steps * (0.7 + 0.002 * g.MT) + ends;
+                    const double shared = steps * (1.1 + 0.004 * g.MT) + ends, alone = steps * (0.7 + 0.002 * g.MT) + ends;
                     cost = (double)full * shared + (rest == 0 ? 0.0 : rest <= slots ? alone : shared);
                 }
                 if (best->cost < 0 || cost < best->cost * 0.98) {

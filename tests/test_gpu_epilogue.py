@@ -192,3 +192,22 @@ def test_refusals():
         lin.spmm_ep(torch.zeros((4, 129), dtype=torch.float16, device="cuda")[:, :128])
     with pytest.raises(spw.SpwError):
         lin.spmv_ep(half(17, 128, "x"))
+
+
+@pytest.mark.parametrize("name", ref64.ACTS)
+def test_activation_of_every_finite_value(name):
+    """Weight = identity, so the product is the operand itself: every finite fp16 through the
+    activation of both products.  Bound: half a step, and 2^-16 of the value.  (Wherever the
+    result is not below 2^-25, the exponentials' arguments stay below 18; five fp32 roundings
+    of one are 18 * 5 * 2^-24 < 5.4e-6 of its exponential, __expf's own error (2 + 18) 2^-23 <
+    2.4e-6, the normal tail's fit 1.3e-6, divisions and products a few 2^-23: 1.1e-5 < 2^-16.)"""
+    eye = torch.eye(64, device="cuda")
+    lin = spw.SparseLinear(eye.to(torch.float16), eye.to(torch.uint8))
+    bits = torch.arange(65536, dtype=torch.int32, device="cuda")
+    x = bits[(bits & 0x7C00) != 0x7C00].to(torch.int16).view(torch.float16).view(-1, 64)
+    a, _ = ref64.act(x.double(), name)
+    bound = (ref64.HALF + 2.0 ** -16) * a.abs() + ref64.TINY
+    ref64.assert_within(lin.spmm_ep(x, act=name), a, bound, "spmm_ep " + name)
+    for i in range(0, x.shape[0], 16):
+        ref64.assert_within(lin.spmv_ep(x[i:i + 16], act=name), a[i:i + 16], bound[i:i + 16], "spmv_ep " + name)
+    ok()
