@@ -1089,15 +1089,21 @@ class SparseLinear:
     def spmm_tokens(self, X, threshold=0.0, Y=None, ws=None, stream=None):
         return spw_spmm_tokens(self.hdr, self.buf, X, threshold, Y, ws, stream=stream)
 
+    @_on_stream
     def spmv_ep(self, x, threshold=0.0, act_bits=None, bias=None, act=SPW_ACT_NONE, residual=None,
-                y=None, stream=None):
+                y=None):
         x2 = x if x.dim() == 2 else x.unsqueeze(0)
-        B = x2.shape[0]
-        if ("ep", B) not in self._ws:
-            need = spw_spmv_ep_workspace_bytes(self.hdr, B)
-            self._ws[("ep", B)] = torch.zeros(need, dtype=torch.uint8, device=self.buf.device) if need else None
-        return spw_spmv_ep(self.hdr, self.buf, x2, threshold, act_bits, bias, act, residual, y,
-                           self._ws[("ep", B)], stream=stream)
+        # A workspace for each batch and stream, so that calls on two streams can overlap.  A
+        # captured call gets its own (cleared by the graph): one that the graph shared with eager
+        # calls or with another graph would be in use twice when they run at once.
+        ws = None
+        if not torch.cuda.is_current_stream_capturing():
+            key = ("ep", x2.shape[0], _stream().value)
+            if key not in self._ws:
+                need = spw_spmv_ep_workspace_bytes(self.hdr, x2.shape[0])
+                self._ws[key] = torch.zeros(need, dtype=torch.uint8, device=self.buf.device) if need else None
+            ws = self._ws[key]
+        return spw_spmv_ep(self.hdr, self.buf, x2, threshold, act_bits, bias, act, residual, y, ws)
 
     def spmm_ep(self, X, bias=None, act=SPW_ACT_NONE, residual=None, Y=None, ws=None, stream=None):
         return spw_spmm_ep(self.hdr, self.buf, X, bias, act, residual, Y, ws, stream=stream)

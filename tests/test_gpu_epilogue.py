@@ -211,3 +211,59 @@ def test_activation_of_every_finite_value(name):
     for i in range(0, x.shape[0], 16):
         ref64.assert_within(lin.spmv_ep(x[i:i + 16], act=name), a[i:i + 16], bound[i:i + 16], "spmv_ep " + name)
     ok()
+
+
+# Long sums of few rows: the reduction is split, and the workspace's counters are in use (the
+# CUDA-core decode at 1 row, the tensor cores at 9).
+@pytest.mark.parametrize("B", [1, 9])
+def test_decode_captured_before_any_call(B):
+    """The first call of a weight is captured; an eager call then comes before the first replay."""
+    lin, W = layer(100, 8200, 0.5, "capture")
+    x, y0 = half(B, 8200, "cap", B), torch.empty(B, 100, dtype=torch.float16, device="cuda")
+    want = ref64.epilogue(*ref64.product(x, W), "silu")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lin.spmv_ep(x, act="silu", y=y0)
+    for _ in range(2):
+        ref64.assert_within(lin.spmv_ep(x, act="silu"), *want)
+        y0.zero_()
+        graph.replay()
+        ref64.assert_within(y0, *want)
+    ok()
+
+
+@pytest.mark.parametrize("B", [1, 9])
+def test_decode_on_two_streams_and_in_two_graphs(B):
+    """Calls of one weight that overlap: eager ones on two streams, then two graphs."""
+    lin, W = layer(100, 8200, 0.5, "streams")
+    xs = [half(B, 8200, "two", B, i) for i in range(2)]
+    want = [ref64.epilogue(*ref64.product(x, W), "relu") for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    ys = [torch.zeros(20, B, 104, dtype=torch.float16, device="cuda")[:, :, :100] for _ in xs]  # 16-byte rows
+    torch.cuda.synchronize()
+    for r in range(20):
+        for x, y, s in zip(xs, ys, streams):
+            lin.spmv_ep(x, act="relu", y=y[r], stream=s)
+    torch.cuda.synchronize()
+    for y, (a, bound) in zip(ys, want):
+        ref64.assert_within(y, a.expand_as(y), bound.expand_as(y))
+    graphs = [torch.cuda.CUDAGraph() for _ in xs]
+    for g, x, y in zip(graphs, xs, ys):
+        y.zero_()
+        with torch.cuda.graph(g):
+            for r in range(20):
+                lin.spmv_ep(x, act="relu", y=y[r])
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for y, (a, bound) in zip(ys, want):
+        ref64.assert_within(y, a.expand_as(y), bound.expand_as(y))
+    ok()
+
+
+def test_decode_splits_at_these_sizes():
+    lin, _ = layer(100, 8200, 0.5, "streams")
+    assert spw.spw_spmv_ep_workspace_bytes(lin.hdr, 1) > 0
