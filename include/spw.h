@@ -519,7 +519,9 @@ int spw_spmv_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, i
  * few rows the compressed weight is decoded into shared memory; for many it is first expanded
  * to dense fp16 in the workspace (at least 2 N K bytes then, rows and columns rounded up).  A
  * dropped weight is an explicit zero in both, so a non-finite X entry reaches every column of
- * its row, as in spw_spmm.  M >= 0 (M == 0 does nothing).
+ * its row, as in spw_spmm.  M >= 0 (M == 0 does nothing); M, N and K up to 2^31 - 4096.
+ * Here and in the three calls below an output overlaps no input (but for the residual) and no
+ * other output; equal pointers are refused where a call has several outputs of a kind.
  * Workspace of this call and of the three below: spw_..._workspace_bytes(..., M) bytes (0: d_ws
  * may be NULL), 16-byte aligned, of any content; nothing is kept in it between calls.  Calls
  * that may run at the same time must not share one.  Deterministic.  Asynchronous.  Errors:

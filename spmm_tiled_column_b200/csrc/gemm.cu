@@ -979,6 +979,7 @@ bool choose_direct(int mode, const spw_format* h, const spw_format* h2, int M, c
 
 // h2: the second weight's header, or null.
 int make_layout(const spw_format* h, const spw_format* h2, int M, int what, Layout* L) {
+    if (M > kMaxDim || h->N > kMaxDim || h->K > kMaxDim) return SPW_ERR_UNSUPPORTED;
     const int pairs = gemm_pairs();
     const int weights = h2 ? 2 : 1;
     memset(L, 0, sizeof(*L));
@@ -1246,6 +1247,7 @@ int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_f
     if (!aligned16(d_buf_gate) || !aligned16(d_buf_up) || !aligned16(d_X) || !aligned16(d_H) || !aligned16(d_G) ||
         !aligned16(d_U))
         return SPW_ERR_ALIGNMENT;
+    if (d_G && (d_G == d_U || d_G == d_H || d_U == d_H)) return SPW_ERR_INVALID_ARG;
     Layout L;
     rc = make_layout(hdr_gate, hdr_up, M, kForward, &L);
     if (rc == SPW_OK) rc = check_ws(d_ws, ws_bytes, L);
@@ -1288,6 +1290,10 @@ int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate, co
     if (!aligned16(d_buf_gate) || !aligned16(d_buf_up) || !aligned16(d_X) || !aligned16(d_G) || !aligned16(d_U) ||
         !aligned16(d_dH) || !aligned16(d_dX) || !aligned16(d_dV_gate) || !aligned16(d_dV_up))
         return SPW_ERR_ALIGNMENT;
+    // (with nothing kept a gradient has no entries, and any address stands for it)
+    if (d_dV_gate && d_dV_gate == d_dV_up && hdr_gate->bytes_total > hdr_gate->off_values &&
+        hdr_up->bytes_total > hdr_up->off_values)
+        return SPW_ERR_INVALID_ARG;
     cudaStream_t s = (cudaStream_t)stream;
     if (M == 0) {  // no token: the kept weights' gradient is zero
         if (d_dV_gate) {

@@ -624,6 +624,7 @@ int resident(int groups, int parts) {
 
 int search_plan(int mode, const spw_format* h, const spw_format* h2, int M, uint32_t units, DirectPlan* best) {
     best->cost = -1.0;
+    if (M > kMaxDim || h->N > kMaxDim || h->K > kMaxDim) return SPW_ERR_UNSUPPORTED;
     for (int groups = 2; groups <= 4; groups += 2)
         for (int cap = kMaxTok; cap >= 64; cap /= 2) {
             DirectPlan g;

@@ -25,6 +25,10 @@ struct PrefillOut {
     int rows, cols;  // of the result (kFfn: of H)
 };
 
+// Largest M, N and K of these products: rows and columns are numbered in int up to the end of the
+// last tile (at most 512 past the last row).
+constexpr long long kMaxDim = 0x7ffff000;
+
 // A product by the direct form: the weights (h2 null for one), the activations of each
 // segment (kDx: dY of each weight; else one), their row strides in bytes.
 struct DirectCall {

@@ -125,3 +125,22 @@ def test_activation_names(spw):
     assert ctypes.sizeof(spw.spw_epilogue) == 24
     with pytest.raises(ValueError):
         spw._act("swish")
+
+
+def test_equal_outputs_and_largest_sizes(spw):
+    L, h = spw.lib(), valid_header(spw)
+    UNSUPPORTED = 5
+    A, B, C = (P(0x10000 * i) for i in (2, 3, 4))
+
+    def f(H, G, U):
+        return L.spw_spmm_ffn(by(h), GOOD, by(h), GOOD, GOOD, 4, 128, 2, H, 128, G, 128, U, 128, GOOD, WS, S)
+
+    assert f(A, B, B) == INVALID and f(A, A, B) == INVALID and f(A, B, A) == INVALID
+    assert h.bytes_total > h.off_values
+    assert L.spw_spmm_ffn_backward(by(h), GOOD, by(h), GOOD, GOOD, 4, 128, 2, GOOD, 128, GOOD, 128, GOOD, 128, A, 128,
+                                   B, B, GOOD, WS, S) == INVALID
+    M = 0x7ffff001  # the last tile's rows would pass 2^31
+    assert L.spw_spmm_ep(by(h), GOOD, GOOD, M, 128, None, A, 128, GOOD, WS, S) == UNSUPPORTED
+    assert L.spw_spmm_ffn(by(h), GOOD, by(h), GOOD, GOOD, M, 128, 2, A, 128, B, 128, C, 128, GOOD, WS, S) == UNSUPPORTED
+    assert L.spw_spmm_backward(by(h), GOOD, GOOD, M, 128, GOOD, 128, A, 128, B, GOOD, WS, S) == UNSUPPORTED
+    assert L.spw_spmm_ep_workspace_bytes(by(h), M) == 0
