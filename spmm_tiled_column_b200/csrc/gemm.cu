@@ -5,12 +5,17 @@
 //   spw_spmm_ffn_backward  dX = dG Wg + dU Wu, and dG^T X, dU^T X at the kept positions
 //   spw_spmm_backward      dX = dY W, and dY^T X at the kept positions
 //
+// For few tokens these calls take the direct form of spmm_direct.cu instead (choose_direct); the
+// gradients of kept weights are computed here alone.
+//
 // Why expanded: spmm.cu decodes each weight tile into shared memory once per token tile, and
 // the decode, the operand's stores and the MMA's reads then share one SM's shared-memory
 // bandwidth.  Here expand_kernel writes the dense weight once into the workspace (a
 // write of 2 N K bytes, most of it still in L2 when it is read), and the product runs as a
 // plain dense GEMM whose operands come by TMA alone; a gradient needs the weight along its
-// other dimension, which the same expanded copy serves as an MN-major operand.
+// other dimension, which the same expanded copy serves as an MN-major operand.  Bound by the
+// tensor cores: 4096 x 4096 at 4096 tokens 101 us (1360 TFLOP/s; a dense library product 95),
+// 4096 x 11008 at 2048 tokens 138 us (121), and 12 and 27 us for their expansion.
 //
 // The product: a cluster of two CTAs (an SM pair) computes a 256 x BN tile (BN = 256 or 128)
 // with tcgen05.mma.cta_group::2: each CTA holds 128 rows of A, half of B and 128 rows of the

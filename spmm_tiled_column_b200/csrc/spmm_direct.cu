@@ -4,20 +4,23 @@
 //   kEp   Y = act(X W^T + bias) + residual     A = 128 weight rows (two strips)
 //   kFfn  H = act(X Wg^T) * (X Wu^T)           A = 64 gate rows, then the same 64 up rows
 //   kDx   dX = sum over the weights of dY W    A = 128 weight columns (two k-tiles), MN-major
-//   kDecode  as kEp for at most 16 rows, with the decode's threshold rule and column set
+//   kDecode  as kEp for at most 16 rows, with the decode's threshold rule or column set
 //
 // With few tokens each weight tile is needed once or twice, so what bounds the product is the
-// decoding (about 900 warp instructions and 300 shared-memory wavefronts for a 64 x 64 tile)
-// and, for small weights, the latency of the chain pointers -> compressed tile -> decode ->
-// MMA -> result.  The design follows from that:
+// decoding (about 900 warp instructions and 400 shared-memory wavefronts for a 64 x 64 tile, of
+// which an SM does two in 0.58 us) and, for small weights, the latency of the chain pointers ->
+// compressed tile -> decode -> MMA -> result (6.3 us for one tile).  At 50 %: 4096 x 4096 with an
+// epilogue 16.2 us at 16 tokens, 19.2 at 128; 4096 x 11008 32 and 36; 11008 x 4096 gated 66 and 77.
+// The design follows from that:
 //   * A CTA computes 128 x MT (MT tokens, at most 512; fp32 accumulator in tensor memory)
 //     over one of `parts` pieces of the reduction; the pieces of a tile form a cluster, which
 //     adds them through distributed shared memory: no workspace, no counters, every CTA of the
 //     cluster finishes its share of the tokens.  Summed in piece order (deterministic).
 //   * Decoders work in groups of four warps, each group on a step (two 64 x 64 tiles) of its
 //     own, a warp on 32 columns of one tile: the waits, scans and look-ups of the groups
-//     overlap.  A step's dense tiles are stored as core matrices of 8 rows x 16 bytes (no
-//     swizzle), which the MMA takes K-major (kEp, kFfn) or MN-major (kDx) from the same bytes.
+//     overlap.  A CTA has four groups, or two where two such CTAs an SM fit the grid better.
+//     A step's dense tiles are stored as core matrices of 8 rows x 16 bytes (no swizzle),
+//     which the MMA takes K-major (kEp, kFfn) or MN-major (kDx) from the same bytes.
 //   * warp 0: TMA of the token tiles (kDecode: loads them itself and applies the rule on the
 //     way into shared memory); warp 1: MMAs; warp 2: tile pointers (16 steps at a time,
 //     ahead) and bulk copies of the compressed tiles; warps 3..: decoders.
@@ -221,12 +224,13 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
             // Rows with the rule applied, written where TMA would put them (128-byte swizzle).  A
             // lane has four 16-byte chunks of the 16 x 64 tile: rows lane / 8 + 4 i, columns 8 c ..
             // On fp16 values |v| < t is a comparison of magnitude bits with those of the smallest
-            // fp16 not below t (p.t_bits, at least 1: an exact zero is dropped, NaN is kept).
+            // fp16 not below t (p.t_bits, at least 1: an exact zero is dropped, NaN is kept); with
+            // the sign bits set, two subtractions in one word borrow nothing from each other.
             const int c = lane & 7, r0 = lane >> 3;
             const uint32_t tb = p.t_bits | p.t_bits << 16;
-            const bool ruled = p.t_bits > 1 || p.act_bits;  // else only zeros are dropped
-            uint4 v[4], vn[4];
-            uint32_t on = 0xFFu, on_n = 0xFFu;
+            // Two steps at a time under one proxy fence, the next two on their way meanwhile.
+            uint4 v[2][4];
+            uint32_t on[2] = {0xFFu, 0xFFu};
             auto fetch = [&](int k, uint4 (&to)[4], uint32_t& bits) {
                 const int col = kBK * k + 8 * c;
 #pragma unroll
@@ -237,39 +241,49 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
                 bits = p.act_bits && col < p.K ? __ldg(p.act_bits + (col >> 5)) >> (col & 31) : 0xFFu;
                 if (col + 8 > p.K) bits &= (1u << max(p.K - col, 0)) - 1u;
             };
-            fetch(k0, v, on);
-            for (int n = 0, slot = 0; n < nk; n++) {
-                if (n + 1 < nk) fetch(k0 + n + 1, vn, on_n);
-                const int last = n - p.sx;
-                if (last >= 0 && !__all_sync(0xffffffffu, wait_or_abort(smem_u32(&x_empty[last % kRing]),
-                                                                        (uint32_t)(last / kRing) & 1u, abort_flag, p.wait_limit))) {
-                    if (lane == 0) flag_abort(abort_flag, p.status);
-                    break;
-                }
-                unsigned char* dst = smem + (uint32_t)slot * p.x_bytes;
-                const bool cut = ruled || kBK * (k0 + n + 1) > p.K;  // warp-uniform
-                uint32_t m[4];
+            fetch(k0, v[0], on[0]);
+            if (nk > 1) fetch(k0 + 1, v[1], on[1]);
+            int slot = 0;
+            bool ok = true;
+            for (int n = 0; n < nk && ok; n += 2) {
 #pragma unroll
-                for (int e = 0; e < 4; e++)  // columns 2e, 2e+1 of the chunk
-                    m[e] = ((on >> (2 * e)) & 1u ? 0x0000FFFFu : 0u) | ((on >> (2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    if (4 * i >= p.B && n >= p.sx) break;  // rows past the last stay zero
-                    const int r = r0 + 4 * i;
-                    uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    if (cut) {
-#pragma unroll
-                        for (int e = 0; e < 4; e++) w[e] &= m[e] & __vcmpgeu2(w[e] & 0x7FFF7FFFu, tb);
+                for (int j = 0; j < 2; j++) {
+                    const int last = n + j - p.sx;
+                    if (n + j >= nk) break;
+                    if (last >= 0 && !__all_sync(0xffffffffu, wait_or_abort(smem_u32(&x_empty[last % kRing]),
+                                                                            (uint32_t)(last / kRing) & 1u, abort_flag,
+                                                                            p.wait_limit))) {
+                        if (lane == 0) flag_abort(abort_flag, p.status);
+                        ok = false;
+                        break;
                     }
-                    *(uint4*)(dst + 128 * r + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    unsigned char* dst = smem + (uint32_t)slot * p.x_bytes;
+                    uint32_t m[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++)  // columns 2e, 2e+1 of the chunk
+                        m[e] = ((on[j] >> (2 * e)) & 1u ? 0x0000FFFFu : 0u) | ((on[j] >> (2 * e + 1)) & 1u ? 0xFFFF0000u : 0u);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        if (4 * i >= p.B && n + j >= p.sx) break;  // rows past the last stay zero
+                        const int r = r0 + 4 * i;
+                        uint32_t w[4] = {v[j][i].x, v[j][i].y, v[j][i].z, v[j][i].w};
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const uint32_t ge = (w[e] | 0x80008000u) - tb;  // bits 15 and 31: not below t
+                            w[e] &= m[e] & prmt(ge, ge, 0xBB99u);
+                        }
+                        *(uint4*)(dst + 128 * r + ((c ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                    if (n + j + 2 < nk) fetch(k0 + n + j + 2, v[j], on[j]);
+                    if (++slot == p.sx) slot = 0;
                 }
+                if (!ok) break;
                 fence_proxy_async_smem();  // generic stores -> tensor-core reads
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&x_full[n % kRing]));
-#pragma unroll
-                for (int i = 0; i < 4; i++) v[i] = vn[i];
-                on = on_n;
-                if (++slot == p.sx) slot = 0;
+                if (lane == 0) {
+                    mbar_arrive(smem_u32(&x_full[n % kRing]));
+                    if (n + 1 < nk) mbar_arrive(smem_u32(&x_full[(n + 1) % kRing]));
+                }
             }
         } else if (lane == 0) {  // --------------------------------- token tiles
             for (int n = 0, slot = 0; n < nk; n++) {

@@ -1308,8 +1308,8 @@ int spw_spmv_ep_path(const spw_format* hdr, int B) {
     if (check_header(hdr) != SPW_OK || B < 1 || B > 16) return -1;
     // The CUDA-core decode's time grows with every row, and with the pieces of a strip that its
     // last warp adds up row by row; the tensor cores' hardly does.  Measured at 50 % (us, 1 / 4 /
-    // 8 rows, against tensor cores): 1000 x 1000 7.0 / 10.5 / 15 against 8.0; 512 x 8192 10 / 21 /
-    // 39 against 17; 4096 x 4096 12 / 19 / 30 against 17; 11008 x 4096 20 / 29 / 43 against 42.
+    // 8 rows, against tensor cores): 1000 x 1000 6.9 / 9.9 / 14 against 7.9; 512 x 8192 10 / 20 /
+    // 38 against 16; 4096 x 4096 11 / 18 / 30 against 16; 11008 x 4096 19 / 28 / 44 against 34.
     const double entries = 1e-6 * (double)hdr->N * hdr->K;
     double pieces = 2368.0 / hdr->n_strips;
     if (pieces > hdr->n_ktiles) pieces = hdr->n_ktiles;
@@ -1334,12 +1334,15 @@ int spw_spmv_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_x, i
     if (spw_spmv_ep_path(hdr, B) == 1) {
         DirectCall c;
         memset(&c, 0, sizeof(c));
-        c.mode = kDecode;
+        // without a threshold and a column set the rule drops exact zeros alone, and the rows go
+        // by TMA as in prefill
+        c.mode = threshold > 0.0f || d_act_bits ? kDecode : kEp;
         c.h[0] = hdr;
         c.buf[0] = d_buf;
         c.x[0] = d_x;
         c.M = B;
         c.ldx = ldx;
+        c.ldx_bytes[0] = 2ull * (B > 1 ? (uint64_t)ldx : round_up_u64((uint64_t)ldx, 8));
         c.t = threshold;
         c.act_bits = d_act_bits;
         c.out.rows = B;

@@ -267,3 +267,26 @@ def test_decode_on_two_streams_and_in_two_graphs(B):
 def test_decode_splits_at_these_sizes():
     lin, _ = layer(100, 8200, 0.5, "streams")
     assert spw.spw_spmv_ep_workspace_bytes(lin.hdr, 1) > 0
+
+
+@pytest.mark.parametrize("B", [2, 16])
+def test_decode_threshold_boundaries(B):
+    """Weight = identity: the result is x~ itself.  Thresholds at, just above and just below fp16
+    values, below the smallest and above the largest one; non-finite entries only where the column
+    set is off (there they must leave no trace, on the tensor cores either)."""
+    eye = torch.eye(64, device="cuda")
+    lin = spw.SparseLinear(eye.to(torch.float16), eye.to(torch.uint8))
+    assert spw.spw_spmv_ep_path(lin.hdr, 16) == 1 and spw.spw_spmv_ep_path(lin.hdr, 2) == 0
+    base = torch.tensor([0.5, 0.4998, 0.50049, 6e-8, 1.2e-7, 6.1e-5, 6.2e-5, 65504.0, 65472.0, 1.0, 0.0, -0.0, 2.0,
+                         1e-4, 3.0, 0.25], dtype=torch.float16, device="cuda")
+    x = torch.stack([base.repeat(4).roll(b) * (1 if b % 2 else -1) for b in range(B)])
+    on = torch.ones(64, dtype=torch.bool, device="cuda")
+    on[[3, 17, 40]] = False
+    x[:, 3], x[:, 17], x[:, 40] = float("nan"), float("inf"), 1.0
+    words = (on.view(2, 32).long() << torch.arange(32, device="cuda")).sum(1)
+    words = torch.where(words >= 2 ** 31, words - 2 ** 32, words).to(torch.int32)
+    for t in (0.0, 1e-9, 6e-8, 5.96e-8, 6.1e-5, 0.5, 0.50001, 0.49999, 1.0, 65504.0, 65503.9, 1e6):
+        keep = on & ~(x.double().abs() < float(np.float32(t)))
+        want = torch.where(keep, x.double(), torch.zeros((), dtype=torch.float64, device="cuda"))
+        assert torch.equal(lin.spmv_ep(x, t, words).double(), want), t
+    ok()
