@@ -960,7 +960,10 @@ uint64_t map_ld(int ld, int rows) { return 2ull * (rows > 1 ? (uint64_t)ld : rou
 
 
 // Workspace sections: the split counters of each product, the expanded weights, dG and dU
-// where there are any, and the fp32 partials.
+// where there are any, and the fp32 partials.  They start at the workspace's first multiple of
+// kWsAlign (the expansion stores 32 bytes at a time, and the caller's pointer need only be a
+// multiple of 16), so `total` holds what that may skip.
+constexpr uint64_t kWsAlign = 256;
 struct Layout {
     GemmPlan fwd, dx, dv;
     bool fwd_direct, dx_direct;  // by the direct form (spmm_direct.cu): no workspace
@@ -1026,8 +1029,12 @@ int make_layout(const spw_format* h, const spw_format* h2, int M, int what, Layo
         weights == 2 && (what & (kDxOut | kDvOut)) ? 2 * round_up_u64(2ull * (uint64_t)M * L->ldn, 256) : 0;
     L->partials = L->grads + grads;
     L->total = L->partials + part;
+    if (L->total) L->total += kWsAlign - 16;
     return SPW_OK;
 }
+
+// Where the sections of a checked workspace start (null stays null: nothing is read then).
+uint8_t* ws_base(void* d_ws) { return (uint8_t*)(((uintptr_t)d_ws + kWsAlign - 1) & ~(uintptr_t)(kWsAlign - 1)); }
 
 int check_ws(const void* d_ws, uint64_t ws_bytes, const Layout& L) {
     if (!L.total) return SPW_OK;
@@ -1222,7 +1229,7 @@ int spw_spmm_ep(const spw_format* hdr, const void* d_buf, const uint16_t* d_X, i
         o.ldr = ep->ldr;
     }
     o.vec = vec_bits(o);
-    return run_forward<kEp>(L, &hdr, &d_buf, d_X, M, ldx, o, (uint8_t*)d_ws, s);
+    return run_forward<kEp>(L, &hdr, &d_buf, d_X, M, ldx, o, ws_base(d_ws), s);
 }
 
 static int check_ffn_pair(const spw_format* hg, const spw_format* hu) {
@@ -1272,7 +1279,7 @@ int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_f
     o.vec = vec_bits(o);
     const spw_format* hdrs[2] = {hdr_gate, hdr_up};
     const void* bufs[2] = {d_buf_gate, d_buf_up};
-    return run_forward<kFfn>(L, hdrs, bufs, d_X, M, ldx, o, (uint8_t*)d_ws, s);
+    return run_forward<kFfn>(L, hdrs, bufs, d_X, M, ldx, o, ws_base(d_ws), s);
 }
 
 uint64_t spw_spmm_ffn_backward_workspace_bytes(const spw_format* hdr_gate, const spw_format* hdr_up, int M) {
@@ -1315,7 +1322,7 @@ int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate, co
     rc = make_layout(hdr_gate, hdr_up, M, kDxOut | kDvOut, &L);
     if (rc == SPW_OK) rc = check_ws(d_ws, ws_bytes, L);
     if (rc != SPW_OK) return rc;
-    uint8_t* ws = (uint8_t*)d_ws;
+    uint8_t* ws = ws_base(d_ws);
     uint16_t* dG = (uint16_t*)(ws + L.grads);
     uint16_t* dU = (uint16_t*)(ws + L.grads + round_up_u64(2ull * (uint64_t)M * L.ldn, 256));
     const long long n = (long long)M * ((N + 7) / 8);
@@ -1369,7 +1376,7 @@ int spw_spmm_backward(const spw_format* hdr, const void* d_buf, const uint16_t* 
     rc = make_layout(hdr, nullptr, M, kDxOut | kDvOut, &L);
     if (rc == SPW_OK) rc = check_ws(d_ws, ws_bytes, L);
     if (rc != SPW_OK) return rc;
-    uint8_t* ws = (uint8_t*)d_ws;
+    uint8_t* ws = ws_base(d_ws);
     uint32_t* counters = (uint32_t*)ws;
     const uint64_t ld_bytes[1] = {map_ld(lddy, M)};
     if (L.counters) SPW_CUDA_TRY(cudaMemsetAsync(ws, 0, L.counters, s));
