@@ -191,7 +191,18 @@ def _rows(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
         t = t.unsqueeze(0)
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
-    return t, max(t.stride(0), t.shape[1])
+    return t, _ld(t, name)
+
+
+def _ld(t: torch.Tensor, name: str) -> int:
+    """Leading dimension of a 2-D view with unit column stride.  The library steps from row to
+    row by it, so rows that overlap (a broadcast, a sliding window) cannot be handed over."""
+    m, n = t.shape
+    ld = t.stride(0)
+    if m > 1 and ld < n:
+        raise ValueError(f"{name} is {m} x {n} with rows {ld} elements apart: they overlap "
+                         "(make it contiguous)")
+    return max(ld, n)
 
 
 def _need(t: torch.Tensor, rows: int, cols: int, name: str):
@@ -813,7 +824,7 @@ def _mat(t: torch.Tensor, rows: int | None, cols: int, name: str) -> tuple[torch
     if n != cols or (rows is not None and m != rows):
         raise ValueError(f"{name} is {m} x {n}; the call takes {'any' if rows is None else rows} rows of "
                          f"{cols} columns")
-    return t, m, max(t.stride(0), n)
+    return t, m, _ld(t, name)
 
 
 def _out(t: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, name: str):

@@ -1,0 +1,40 @@
+"""Rows handed to the library as a pointer and a leading dimension: views whose rows overlap (a
+broadcast, a sliding window) are refused, on the host."""
+import pytest
+import torch
+
+import spmm_tiled_column_b200 as spw
+
+
+def half(*shape):
+    return torch.zeros(*shape, dtype=torch.float16)
+
+
+def overlapping():
+    row = half(64)
+    return {
+        "broadcast": row.expand(10, 64),              # 128 bytes that would be read as 1280
+        "gradient of a sum over rows": half(1, 64).expand(10, 64),
+        "sliding window": half(100).unfold(0, 64, 4),  # 10 rows, 4 elements apart
+        "one short": half(10 * 64).as_strided((10, 64), (63, 1)),
+    }
+
+
+@pytest.mark.parametrize("which", list(overlapping()))
+def test_overlapping_rows_are_refused(which):
+    t = overlapping()[which]
+    assert t.shape == (10, 64) and t.stride(1) == 1
+    with pytest.raises(ValueError, match="overlap"):
+        spw._mat(t, None, 64, "residual")
+    with pytest.raises(ValueError, match="overlap"):
+        spw._rows(t, "Y")
+
+
+def test_single_rows_and_padded_rows_are_taken():
+    for t, rows, ld in ((half(64), 1, 64), (half(1, 64).expand(1, 64), 1, 64), (half(64).as_strided((1, 64), (0, 1)), 1, 64),
+                        (half(10, 72)[:, :64], 10, 72), (half(10, 64), 10, 64), (half(0, 64), 0, 64),
+                        (half(20, 64)[::2], 10, 128)):
+        v, m, got = spw._mat(t, None, 64, "x")
+        assert (m, got, v.shape) == (rows, ld, (rows, 64))
+        v, got = spw._rows(t, "x")
+        assert got == ld and v.shape == (rows, 64)
