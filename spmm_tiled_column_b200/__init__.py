@@ -194,6 +194,9 @@ def _rows(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
     return t, _ld(t, name)
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
 def _ld(t: torch.Tensor, name: str) -> int:
     """Leading dimension of a 2-D view with unit column stride.  The library steps from row to
     row by it, so rows that overlap (a broadcast, a sliding window) cannot be handed over."""
@@ -202,7 +205,10 @@ def _ld(t: torch.Tensor, name: str) -> int:
     if m > 1 and ld < n:
         raise ValueError(f"{name} is {m} x {n} with rows {ld} elements apart: they overlap "
                          "(make it contiguous)")
-    return max(ld, n)
+    if m > 1 and max(m, ld) > _INT_MAX:  # M and ld are C ints, and ctypes cuts to 32 bits
+        raise ValueError(f"{name} is {m} x {n} with rows {ld} elements apart: the library counts both "
+                         f"up to {_INT_MAX}")
+    return n if ld > _INT_MAX else max(ld, n)  # (a single row: any stride)
 
 
 def _need(t: torch.Tensor, rows: int, cols: int, name: str):

@@ -38,3 +38,24 @@ def test_single_rows_and_padded_rows_are_taken():
         assert (m, got, v.shape) == (rows, ld, (rows, 64))
         v, got = spw._rows(t, "x")
         assert got == ld and v.shape == (rows, 64)
+
+
+def meta(rows, cols, ld):
+    """A view without storage: sizes and strides alone."""
+    return torch.empty(0, dtype=torch.float16, device="meta").as_strided((rows, cols), (ld, 1))
+
+
+@pytest.mark.parametrize("rows,ld", [(2, 2 ** 31), (2, 2 ** 32 + 64), (2 ** 31, 64), (2 ** 32 + 5, 64)])
+def test_sizes_past_31_bits_are_refused(rows, ld):
+    # the library's M and ld are C ints, and ctypes keeps the low 32 bits of what it is given
+    with pytest.raises(ValueError, match="2147483647"):
+        spw._mat(meta(rows, 64, ld), None, 64, "X")
+    with pytest.raises(ValueError, match="2147483647"):
+        spw._rows(meta(rows, 64, ld), "Y")
+
+
+def test_largest_sizes_and_a_single_row_of_any_stride():
+    assert spw._mat(meta(2 ** 31 - 1, 64, 64), None, 64, "X")[1:] == (2 ** 31 - 1, 64)
+    assert spw._mat(meta(2, 64, 2 ** 31 - 8), None, 64, "X")[2] == 2 ** 31 - 8
+    assert spw._mat(meta(1, 64, 2 ** 33), None, 64, "X")[1:] == (1, 64)
+    assert spw._rows(meta(1, 64, 2 ** 33), "Y")[1] == 64
