@@ -805,6 +805,14 @@ def _same_device(*tensors):
                              f"device is cuda:{dev}")
 
 
+def _whole(**tensors):
+    """Raw buffers go over as a pointer and a number of bytes, so a tensor with gaps or repeats
+    (whose storage holds other or fewer bytes than its size says) cannot."""
+    for name, t in tensors.items():
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
 def _on_stream(fn):
     """Gives a call its `stream` keyword.  The call runs with that stream current, so that what
     it allocates belongs to the stream that uses it."""
@@ -907,6 +915,7 @@ def spw_spmv_ep(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
     h = _hdr(hdr)
     x2, B, ldx = _mat(x, None, h.K, "x")
     _same_device(x, buf, act_bits, bias, residual, y, ws)
+    _whole(buf=buf, act_bits=act_bits, ws=ws)
     ep = _epilogue(bias, act, residual, B, h.N)
     _need_buf(buf, h)
     _need_words(act_bits, h.K)
@@ -936,6 +945,7 @@ def spw_spmm_ep(hdr, buf: torch.Tensor, X: torch.Tensor, bias: torch.Tensor | No
     h = _hdr(hdr)
     X2, M, ldx = _mat(X, None, h.K, "X")
     _same_device(X, buf, bias, residual, Y, ws)
+    _whole(buf=buf, ws=ws)
     ep = _epilogue(bias, act, residual, M, h.N)
     _need_buf(buf, h)
     Y, pY, ldy = _out(Y, M, h.N, X, "Y")
@@ -966,6 +976,7 @@ def spw_spmm_ffn(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor,
         raise ValueError("G and U go together")
     save = save or G is not None
     _same_device(X, buf_gate, buf_up, H, G, U, ws)
+    _whole(buf_gate=buf_gate, buf_up=buf_up, ws=ws)
     _need_buf(buf_gate, hg, "buf_gate")
     _need_buf(buf_up, hu, "buf_up")
     H, pH, ldh = _out(H, M, hg.N, X, "H")
@@ -1008,6 +1019,7 @@ def spw_spmm_ffn_backward(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torc
         X2, _, ldx = _mat(X, M, hg.K, "X")
         pX = X2.data_ptr()
     _same_device(G, U, dH, X, buf_gate, buf_up, dX, dV_gate, dV_up, ws)
+    _whole(buf_gate=buf_gate, buf_up=buf_up, ws=ws)
     _need_buf(buf_gate, hg, "buf_gate")
     _need_buf(buf_up, hu, "buf_up")
     pdX, lddx = None, 0
@@ -1044,6 +1056,7 @@ def spw_spmm_backward(hdr, buf: torch.Tensor, X: torch.Tensor | None, dY: torch.
         X2, _, ldx = _mat(X, M, h.K, "X")
         pX = X2.data_ptr()
     _same_device(dY, X, buf, dX, dV, ws)
+    _whole(buf=buf, ws=ws)
     _need_buf(buf, h)
     pdX, lddx = None, 0
     if need_dx:
