@@ -814,10 +814,15 @@ def _whole(**tensors):
 
 
 def _on_stream(fn):
-    """Gives a call its `stream` keyword.  The call runs with that stream current, so that what
-    it allocates belongs to the stream that uses it."""
+    """Gives a call its `stream` argument (by keyword, or after all others).  The call runs with
+    that stream current, so that what it allocates belongs to the stream that uses it, and what it
+    clears is cleared there."""
+    n = fn.__code__.co_argcount
+
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
+        if len(args) == n + 1:
+            args, stream = args[:n], args[n]
         if stream is None:
             return fn(*args, **kw)
         with torch.cuda.stream(stream):
@@ -1071,6 +1076,28 @@ def spw_spmm_backward(hdr, buf: torch.Tensor, X: torch.Tensor | None, dY: torch.
     return dX, dV
 
 
+class _Workspaces:
+    """A holder's zeroed decode workspaces: one for each kind of call, batch and stream, so that
+    calls on two streams can overlap.  A captured call gets its own (cleared by the graph): one
+    that the graph shared with eager calls or with another graph would be in use twice when they
+    run at once, and before the first replay it would not be cleared."""
+
+    def __init__(self, device):
+        self._device, self._held = device, {}
+
+    def get(self, kind: str, B: int, size) -> torch.Tensor | None:
+        """For a call on the current stream; size() gives the bytes (None for 0)."""
+        if torch.cuda.is_current_stream_capturing():
+            return self._new(size())
+        key = kind, B, _stream().value
+        if key not in self._held:
+            self._held[key] = self._new(size())
+        return self._held[key]
+
+    def _new(self, need: int):
+        return torch.zeros(need, dtype=torch.uint8, device=self._device) if need else None
+
+
 class SparseLinear24:
     """A weight held as its 2:4 part (sparse tensor cores) plus a TCB residual: a holder
     for spw_split24, spw_compress and spw_spmm24 (it adds no arithmetic)."""
@@ -1092,6 +1119,7 @@ class SparseLinear:
         self.N, self.K = W.shape
         self.buf, self.hdr = spw_compress(W, mask, stream=stream)
         self._ws = {}
+        self._workspaces = _Workspaces(self.buf.device)
 
     def workspace(self, B: int) -> torch.Tensor:
         if B not in self._ws:
@@ -1123,16 +1151,8 @@ class SparseLinear:
     def spmv_ep(self, x, threshold=0.0, act_bits=None, bias=None, act=SPW_ACT_NONE, residual=None,
                 y=None):
         x2 = x if x.dim() == 2 else x.unsqueeze(0)
-        # A workspace for each batch and stream, so that calls on two streams can overlap.  A
-        # captured call gets its own (cleared by the graph): one that the graph shared with eager
-        # calls or with another graph would be in use twice when they run at once.
-        ws = None
-        if not torch.cuda.is_current_stream_capturing():
-            key = ("ep", x2.shape[0], _stream().value)
-            if key not in self._ws:
-                need = spw_spmv_ep_workspace_bytes(self.hdr, x2.shape[0])
-                self._ws[key] = torch.zeros(need, dtype=torch.uint8, device=self.buf.device) if need else None
-            ws = self._ws[key]
+        B = x2.shape[0]
+        ws = self._workspaces.get("ep", B, lambda: spw_spmv_ep_workspace_bytes(self.hdr, B))
         return spw_spmv_ep(self.hdr, self.buf, x2, threshold, act_bits, bias, act, residual, y, ws)
 
     def spmm_ep(self, X, bias=None, act=SPW_ACT_NONE, residual=None, Y=None, ws=None, stream=None):
@@ -1158,19 +1178,18 @@ class SparseFFN:
         if (gate.N, gate.K) != (up.N, up.K):
             raise ValueError(f"gate is {gate.N} x {gate.K}, up {up.N} x {up.K}")
         self.gate, self.up, self.act = gate, up, _act(act)
-        self._ws = {}
+        self._workspaces = _Workspaces(gate.buf.device)
 
-    def spmv(self, x, threshold=0.0, h=None, act_bits=None, stream=None):
+    @_on_stream
+    def spmv(self, x, threshold=0.0, h=None, act_bits=None):
         """(h, column-set words) of the decode's fused step (SiLU only)."""
         if self.act != SPW_ACT_SILU:
             raise ValueError("the decode form computes SiLU")
         x2 = x if x.dim() == 2 else x.unsqueeze(0)
         B = x2.shape[0]
-        if B not in self._ws:
-            need = spw_spmv_ffn_workspace_bytes(self.gate.hdr, self.up.hdr, B)
-            self._ws[B] = torch.zeros(max(need, 16), dtype=torch.uint8, device=self.gate.buf.device)
+        ws = self._workspaces.get("ffn", B, lambda: max(spw_spmv_ffn_workspace_bytes(self.gate.hdr, self.up.hdr, B), 16))
         return spw_spmv_ffn(self.gate.hdr, self.gate.buf, self.up.hdr, self.up.buf, x2, threshold, h,
-                            act_bits, self._ws[B], stream)
+                            act_bits, ws)
 
     def spmm(self, X, save=False, H=None, G=None, U=None, ws=None, stream=None):
         return spw_spmm_ffn(self.gate.hdr, self.gate.buf, self.up.hdr, self.up.buf, X, self.act, save,
