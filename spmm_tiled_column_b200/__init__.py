@@ -1112,8 +1112,8 @@ class SparseLinear24:
 
 
 class SparseLinear:
-    """A compressed weight with its header and per-batch decode workspaces (a holder for
-    the calls above; it adds no arithmetic)."""
+    """A compressed weight with its header and decode workspaces (a holder for the calls above;
+    it adds no arithmetic)."""
 
     def __init__(self, W: torch.Tensor, mask: torch.Tensor, stream=None):
         self.N, self.K = W.shape
@@ -1122,24 +1122,26 @@ class SparseLinear:
         self._workspaces = _Workspaces(self.buf.device)
 
     def workspace(self, B: int) -> torch.Tensor:
+        """A workspace of spw_spmv for this batch, for callers that pass their own (the methods
+        below hold others)."""
         if B not in self._ws:
             self._ws[B] = torch.zeros(max(spw_spmv_workspace_bytes(self.hdr, B), 16),
                                       dtype=torch.uint8, device=self.buf.device)
         return self._ws[B]
 
-    def spmv(self, x, threshold=0.0, act_bits=None, y=None, stream=None):
-        x2 = x if x.dim() == 2 else x.unsqueeze(0)
-        return spw_spmv(self.hdr, self.buf, x2, threshold, act_bits, y,
-                        self.workspace(x2.shape[0]), stream)
-
-    def spmv_auto(self, x, threshold=0.0, act_bits=None, y=None, stream=None):
+    @_on_stream
+    def spmv(self, x, threshold=0.0, act_bits=None, y=None):
         x2 = x if x.dim() == 2 else x.unsqueeze(0)
         B = x2.shape[0]
-        if ("auto", B) not in self._ws:
-            self._ws[("auto", B)] = torch.zeros(max(spw_spmv_auto_workspace_bytes(self.hdr, B), 16),
-                                                dtype=torch.uint8, device=self.buf.device)
-        return spw_spmv_auto(self.hdr, self.buf, x2, threshold, act_bits, y,
-                             self._ws[("auto", B)], stream)
+        ws = self._workspaces.get("spmv", B, lambda: max(spw_spmv_workspace_bytes(self.hdr, B), 16))
+        return spw_spmv(self.hdr, self.buf, x2, threshold, act_bits, y, ws)
+
+    @_on_stream
+    def spmv_auto(self, x, threshold=0.0, act_bits=None, y=None):
+        x2 = x if x.dim() == 2 else x.unsqueeze(0)
+        B = x2.shape[0]
+        ws = self._workspaces.get("auto", B, lambda: max(spw_spmv_auto_workspace_bytes(self.hdr, B), 16))
+        return spw_spmv_auto(self.hdr, self.buf, x2, threshold, act_bits, y, ws)
 
     def spmm(self, X, Y=None, stream=None):
         return spw_spmm(self.hdr, self.buf, X, Y, stream=stream)

@@ -44,19 +44,38 @@ class Gated:
         assert torch.equal(got.bool(), on)
 
 
+class Plain:
+    """SparseLinear.spmv or spmv_auto."""
+
+    def __init__(self, method, B):
+        self.lin, self.W = layer(N, K, 0.5, "holder")
+        self.method, self.B = getattr(self.lin, method), B
+
+    def out(self):
+        return (torch.zeros(self.B, 104, dtype=torch.float16, device="cuda")[:, :N],)
+
+    def __call__(self, x, out, stream=None):
+        return self.method(x, 0.0, None, out[0], stream=stream)
+
+    def check(self, x, out):
+        z, dz = ref64.product(x, self.W)
+        dz = dz + K * 2.0 ** -24 * (x.double().abs() @ self.W.double().abs().T)
+        ref64.assert_within(out[0], *ref64.epilogue(z, dz, "none"))
+
+
 def make(kind, B):
-    return {"ffn": Gated}[kind](B)
+    return Gated(B) if kind == "ffn" else Plain(kind, B)
 
 
 def inputs(B, n):
     return [half(B, K, "hold", B, i) for i in range(n)]
 
 
-KINDS = ["ffn"]
+KINDS = ["ffn", "spmv", "spmv_auto"]
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B", [1, 9])
+@pytest.mark.parametrize("B", [1, 9, 16])
 def test_captured_before_any_call(kind, B):
     call = make(kind, B)
     (x,) = inputs(B, 1)
@@ -78,7 +97,7 @@ def test_captured_before_any_call(kind, B):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("B", [1, 9])
+@pytest.mark.parametrize("B", [1, 9, 16])
 def test_two_streams_two_graphs_and_a_graph_beside_eager_calls(kind, B):
     call = make(kind, B)
     xs = inputs(B, 2)

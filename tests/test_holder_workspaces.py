@@ -49,7 +49,7 @@ def world(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", on)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: w.capturing)
     monkeypatch.setattr(spw, "_stream", lambda s=None: ctypes.c_void_p(1000 + (w.stream if s is None else s)))
-    for name, place in (("spw_spmv_ffn", 8), ("spw_spmv_ep", 9)):
+    for name, place in (("spw_spmv_ffn", 8), ("spw_spmv_ep", 9), ("spw_spmv", 6), ("spw_spmv_auto", 6)):
         monkeypatch.setattr(spw, name, record(place))
         monkeypatch.setattr(spw, name + "_workspace_bytes", lambda *a: 4096)
     return w
@@ -58,10 +58,10 @@ def world(monkeypatch):
 def call_of(kind):
     if kind == "ffn":
         return spw.SparseFFN(Lin(), Lin()).spmv
-    return Lin().spmv_ep
+    return {"ep": Lin().spmv_ep, "spmv": Lin().spmv, "auto": Lin().spmv_auto}[kind]
 
 
-KINDS = ["ffn", "ep"]
+KINDS = ["ffn", "ep", "spmv", "auto"]
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -90,6 +90,6 @@ def test_a_captured_call_has_its_own(world, kind):
 @pytest.mark.parametrize("kind", KINDS)
 def test_stream_as_the_last_positional_argument(world, kind):
     call = call_of(kind)
-    args = (0.0, None, None) if kind == "ffn" else (0.0, None, None, 0, None, None)
+    args = (0.0, None, None, 0, None, None) if kind == "ep" else (0.0, None, None)
     call(torch.empty(1, K), *args, 7)
     assert world.calls[0][1:] == (7, 7)
