@@ -171,6 +171,23 @@ def _stream(stream=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on_stream(fn):
+    """Gives a call its `stream` argument (by keyword, or after all others).  The call runs with
+    that stream current, so that what it allocates belongs to the stream that uses it, and what it
+    clears is cleared there."""
+    n = fn.__code__.co_argcount
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if len(args) == n + 1:
+            args, stream = args[:n], args[n]
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
@@ -303,19 +320,19 @@ def spw_format_query(mask: torch.Tensor, stream=None) -> tuple[int, int]:
     return nbytes.value, nnz.value
 
 
-def spw_compress(W: torch.Tensor, mask: torch.Tensor, buf: torch.Tensor | None = None,
-                 stream=None) -> tuple[torch.Tensor, spw_format]:
+@_on_stream
+def spw_compress(W: torch.Tensor, mask: torch.Tensor, buf: torch.Tensor | None = None) -> tuple[torch.Tensor, spw_format]:
     """Compress W * mask into a TCB v1 buffer; returns (uint8 device buffer, header)."""
     W, ldw = _rows(_half(W, "W"), "W")
     N, K = W.shape
     mask, ldm = _mask_like(mask, N, K)
     if buf is None:
-        nbytes, _ = spw_format_query(mask, stream)
+        nbytes, _ = spw_format_query(mask)
         buf = torch.empty(nbytes, dtype=torch.uint8, device=W.device)
     hdr = spw_format()
     _check("spw_compress", lib().spw_compress(
         _ptr(W), ldw, _ptr(mask), ldm, N, K, _ptr(buf), _nbytes(buf, "buf"), ctypes.byref(hdr),
-        _stream(stream)))
+        _stream()))
     return buf, hdr
 
 
@@ -326,8 +343,8 @@ def spw_format_read(buf: torch.Tensor, stream=None) -> spw_format:
     return hdr
 
 
-def spw_decompress(hdr, buf: torch.Tensor, out: torch.Tensor | None = None,
-                   stream=None) -> torch.Tensor:
+@_on_stream
+def spw_decompress(hdr, buf: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """Dense masked weight (fp16, N x K) from a TCB v1 buffer."""
     h = _hdr(hdr)
     if out is None:
@@ -336,7 +353,7 @@ def spw_decompress(hdr, buf: torch.Tensor, out: torch.Tensor | None = None,
     _need_buf(buf, h)
     _need(out2, h.N, h.K, "out")
     _check("spw_decompress", lib().spw_decompress(ctypes.byref(h), _ptr(buf), _ptr(out2), ld,
-                                                  _stream(stream)))
+                                                  _stream()))
     return out
 
 
@@ -346,8 +363,9 @@ def _act_words(K: int) -> int:
     return (K + 31) // 32
 
 
+@_on_stream
 def spw_select_threshold(x: torch.Tensor, t: float, act_bits: torch.Tensor | None = None,
-                         count: torch.Tensor | None = None, stream=None):
+                         count: torch.Tensor | None = None):
     """(act_bits int32[ceil(K/32)], count int32[1]) for the threshold rule."""
     x, ldx = _rows(_half(x, "x"), "x")
     B, K = x.shape
@@ -358,12 +376,13 @@ def spw_select_threshold(x: torch.Tensor, t: float, act_bits: torch.Tensor | Non
     _need_words(act_bits, K)
     _need_u32(count, 1, "count")
     _check("spw_select_threshold", lib().spw_select_threshold(
-        _ptr(x), B, K, ldx, float(t), _ptr(act_bits), _ptr(count), _stream(stream)))
+        _ptr(x), B, K, ldx, float(t), _ptr(act_bits), _ptr(count), _stream()))
     return act_bits, count
 
 
+@_on_stream
 def spw_select_topk(x: torch.Tensor, k: int, act_bits: torch.Tensor | None = None,
-                    idx: torch.Tensor | None = None, stream=None):
+                    idx: torch.Tensor | None = None):
     """(act_bits int32[ceil(K/32)], ascending idx int32[k]) of the top-k columns."""
     x, ldx = _rows(_half(x, "x"), "x")
     B, K = x.shape
@@ -374,7 +393,7 @@ def spw_select_topk(x: torch.Tensor, k: int, act_bits: torch.Tensor | None = Non
     _need_words(act_bits, K)
     _need_u32(idx, int(k), "idx")
     _check("spw_select_topk", lib().spw_select_topk(
-        _ptr(x), B, K, ldx, int(k), _ptr(act_bits), _ptr(idx), _stream(stream)))
+        _ptr(x), B, K, ldx, int(k), _ptr(act_bits), _ptr(idx), _stream()))
     return act_bits, idx[:k]
 
 
@@ -385,9 +404,10 @@ def spw_spmv_workspace_bytes(hdr, B: int) -> int:
     return int(lib().spw_spmv_workspace_bytes(ctypes.byref(h), int(B)))
 
 
+@_on_stream
 def spw_spmv(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
              act_bits: torch.Tensor | None = None, y: torch.Tensor | None = None,
-             ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+             ws: torch.Tensor | None = None) -> torch.Tensor:
     """Decode y (B x N fp16) = W_masked . x~ with column skipping.
 
     ws: a zero-initialised uint8 workspace of spw_spmv_workspace_bytes(hdr, B) bytes
@@ -407,7 +427,7 @@ def spw_spmv(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
                          device=x.device)
     _check("spw_spmv", lib().spw_spmv(
         ctypes.byref(h), _ptr(buf), _ptr(x2), B, ldx, float(threshold), _ptr(act_bits),
-        _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream()))
     return y
 
 
@@ -422,8 +442,8 @@ def spw_spmv_group_workspace_bytes(hdrs, B: int) -> int:
     return int(lib().spw_spmv_group_workspace_bytes(len(hdrs), _hdr_array(hdrs), int(B)))
 
 
-def spw_spmv_group(hdrs, bufs, xs, threshold: float = 0.0, act_bits=None, ys=None, ws=None,
-                   stream=None):
+@_on_stream
+def spw_spmv_group(hdrs, bufs, xs, threshold: float = 0.0, act_bits=None, ys=None, ws=None):
     """Decode several layers in one launch; returns the list of outputs (B x N_l each)."""
     n = len(hdrs)
     harr = _hdr_array(hdrs)
@@ -448,13 +468,13 @@ def spw_spmv_group(hdrs, bufs, xs, threshold: float = 0.0, act_bits=None, ys=Non
     _check("spw_spmv_group", lib().spw_spmv_group(
         n, harr, P(*[b.data_ptr() for b in bufs]), P(*[t.data_ptr() for t, _ in x2]),
         I(*[ld for _, ld in x2]), ab, P(*[t.data_ptr() for t, _ in y2]), I(*[ld for _, ld in y2]),
-        B, float(threshold), _ptr(ws), _nbytes(ws), _stream(stream)))
+        B, float(threshold), _ptr(ws), _nbytes(ws), _stream()))
     return ys
 
 
+@_on_stream
 def spw_spmv_noalloc(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
-                     act_bits: torch.Tensor | None = None, y: torch.Tensor | None = None,
-                     stream=None) -> torch.Tensor:
+                     act_bits: torch.Tensor | None = None, y: torch.Tensor | None = None) -> torch.Tensor:
     """Decode like spw_spmv, with the library's own fixed scratch instead of a workspace.
 
     For callers that cannot allocate device memory; see include/spw.h for the size
@@ -471,7 +491,7 @@ def spw_spmv_noalloc(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float =
     _need_words(act_bits, h.K)
     _check("spw_spmv_noalloc", lib().spw_spmv_noalloc(
         ctypes.byref(h), _ptr(buf), _ptr(x2), B, ldx, float(threshold), _ptr(act_bits),
-        _ptr(y2), ldy, _stream(stream)))
+        _ptr(y2), ldy, _stream()))
     return y
 
 
@@ -480,8 +500,9 @@ def spw_spmm_workspace_bytes(hdr, M: int) -> int:
     return int(lib().spw_spmm_workspace_bytes(ctypes.byref(h), int(M)))
 
 
+@_on_stream
 def spw_spmm(hdr, buf: torch.Tensor, X: torch.Tensor, Y: torch.Tensor | None = None,
-             ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+             ws: torch.Tensor | None = None) -> torch.Tensor:
     """Prefill Y (M x N fp16) = X . W_masked^T on tcgen05 tensor cores."""
     h = _hdr(hdr)
     X2, ldx = _rows(_half(X, "X"), "X")
@@ -497,7 +518,7 @@ def spw_spmm(hdr, buf: torch.Tensor, X: torch.Tensor, Y: torch.Tensor | None = N
         ws = torch.zeros(need, dtype=torch.uint8, device=X.device)
     _check("spw_spmm", lib().spw_spmm(
         ctypes.byref(h), _ptr(buf), _ptr(X2), M, ldx, _ptr(Y2), ldy, _ptr(ws),
-        _nbytes(ws), _stream(stream)))
+        _nbytes(ws), _stream()))
     return Y
 
 
@@ -513,8 +534,8 @@ def spw_group_tokens_workspace_bytes(M: int, K: int) -> int:
     return int(lib().spw_group_tokens_workspace_bytes(int(M), int(K)))
 
 
-def spw_group_tokens(X: torch.Tensor, t: float, token_tile: int, ws: torch.Tensor | None = None,
-                     stream=None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+@_on_stream
+def spw_group_tokens(X: torch.Tensor, t: float, token_tile: int, ws: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
     """Token grouping of X (M x K fp16): (Xg M x ceil8(K) fp16, perm int32[M], tile_sig
     int64[ceil(M / token_tile), words]); see spw_group_tokens in include/spw.h."""
     X2, ldx = _rows(_half(X, "X"), "X")
@@ -529,7 +550,7 @@ def spw_group_tokens(X: torch.Tensor, t: float, token_tile: int, ws: torch.Tenso
         ws = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
     _check("spw_group_tokens", lib().spw_group_tokens(
         _ptr(X2), M, K, ldx, ctypes.c_float(t), int(token_tile), _ptr(Xg), ldg, _ptr(perm),
-        _ptr(tsig), _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(tsig), _ptr(ws), _nbytes(ws), _stream()))
     return Xg, perm, tsig
 
 
@@ -545,9 +566,9 @@ def spw_spmm_tokens_plan(hdr, M: int, sm_count: int = 0) -> dict:
     return {name: getattr(info, name) for name, _ in info._fields_}
 
 
+@_on_stream
 def spw_spmm_tokens(hdr, buf: torch.Tensor, X: torch.Tensor, threshold: float,
-                    Y: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-                    stream=None) -> torch.Tensor:
+                    Y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Prefill with per-token index sets: Y = X~ . W_masked^T, tokens grouped by the
     k-tiles they use (see spw_spmm_tokens in include/spw.h).  ws: a uint8 workspace of
     spw_spmm_tokens_workspace_bytes(hdr, M) bytes whose first (split-K counter) bytes are
@@ -566,7 +587,7 @@ def spw_spmm_tokens(hdr, buf: torch.Tensor, X: torch.Tensor, threshold: float,
                          device=X.device)
     _check("spw_spmm_tokens", lib().spw_spmm_tokens(
         ctypes.byref(h), _ptr(buf), _ptr(X2), M, ldx, ctypes.c_float(threshold), _ptr(Y2), ldy,
-        _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(ws), _nbytes(ws), _stream()))
     return Y
 
 
@@ -575,9 +596,10 @@ def spw_spmv_tc_workspace_bytes(hdr, B: int) -> int:
     return int(lib().spw_spmv_tc_workspace_bytes(ctypes.byref(h), int(B)))
 
 
+@_on_stream
 def spw_spmv_tc(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
                 act_bits: torch.Tensor | None = None, y: torch.Tensor | None = None,
-                ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                ws: torch.Tensor | None = None) -> torch.Tensor:
     """Decode y (B x N fp16) on tensor cores; arguments as spw_spmv.  ws: a zero-initialised
     uint8 workspace of spw_spmv_tc_workspace_bytes(hdr, B) bytes (allocated here when
     needed and not given)."""
@@ -596,7 +618,7 @@ def spw_spmv_tc(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
         ws = torch.zeros(need, dtype=torch.uint8, device=x.device)
     _check("spw_spmv_tc", lib().spw_spmv_tc(
         ctypes.byref(h), _ptr(buf), _ptr(x2), B, ldx, float(threshold), _ptr(act_bits),
-        _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream()))
     return y
 
 
@@ -611,9 +633,10 @@ def spw_spmv_auto_workspace_bytes(hdr, B: int) -> int:
     return int(lib().spw_spmv_auto_workspace_bytes(ctypes.byref(h), int(B)))
 
 
+@_on_stream
 def spw_spmv_auto(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
                   act_bits: torch.Tensor | None = None, y: torch.Tensor | None = None,
-                  ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                  ws: torch.Tensor | None = None) -> torch.Tensor:
     """Decode y (B x N fp16) on the path chosen by batch size; arguments as spw_spmv.  ws:
     a zero-initialised uint8 workspace of spw_spmv_auto_workspace_bytes(hdr, B) bytes
     (allocated here when needed and not given)."""
@@ -632,7 +655,7 @@ def spw_spmv_auto(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.
         ws = torch.zeros(need, dtype=torch.uint8, device=x.device)
     _check("spw_spmv_auto", lib().spw_spmv_auto(
         ctypes.byref(h), _ptr(buf), _ptr(x2), B, ldx, float(threshold), _ptr(act_bits),
-        _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(y2), ldy, _ptr(ws), _nbytes(ws), _stream()))
     return y
 
 
@@ -641,10 +664,10 @@ def spw_spmv_ffn_workspace_bytes(hdr_gate, hdr_up, B: int) -> int:
                                                   ctypes.byref(_hdr(hdr_up)), B))
 
 
+@_on_stream
 def spw_spmv_ffn(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor, x: torch.Tensor,
                  threshold: float = 0.0, h: torch.Tensor | None = None,
-                 act_bits: torch.Tensor | None = None, ws: torch.Tensor | None = None,
-                 stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+                 act_bits: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """Fused FFN activation: h (B x N fp16) = SiLU(W_gate x) * (W_up x) and the column-set
     words of h under the threshold rule, in one launch.  ws: a zero-initialised uint8
     workspace of spw_spmv_ffn_workspace_bytes(hdr_gate, hdr_up, B) bytes (allocated here
@@ -667,7 +690,7 @@ def spw_spmv_ffn(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor,
         ws = torch.zeros(max(need, 16), dtype=torch.uint8, device=x.device)
     _check("spw_spmv_ffn", lib().spw_spmv_ffn(
         ctypes.byref(hg), _ptr(buf_gate), ctypes.byref(hu), _ptr(buf_up), _ptr(x2), B, ldx,
-        float(threshold), _ptr(h2), ldh, _ptr(act_bits), _ptr(ws), _nbytes(ws), _stream(stream)))
+        float(threshold), _ptr(h2), ldh, _ptr(act_bits), _ptr(ws), _nbytes(ws), _stream()))
     return h, act_bits
 
 
@@ -740,7 +763,8 @@ def spw_s24_bytes(N: int, K: int) -> int:
     return int(lib().spw_s24_bytes(int(N), int(K)))
 
 
-def spw_split24(W: torch.Tensor, mask: torch.Tensor, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+@_on_stream
+def spw_split24(W: torch.Tensor, mask: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
     """2:4 + residual split: (s24 uint8 buffer of the 2:4 part, residual mask uint8 N x K);
     see spw_split24 in include/spw.h."""
     W2, ldw = _rows(_half(W, "W"), "W")
@@ -749,7 +773,7 @@ def spw_split24(W: torch.Tensor, mask: torch.Tensor, stream=None) -> tuple[torch
     s24 = torch.empty(spw_s24_bytes(N, K), dtype=torch.uint8, device=W.device)
     mask_r = torch.empty((N, K), dtype=torch.uint8, device=W.device)
     _check("spw_split24", lib().spw_split24(_ptr(W2), ldw, _ptr(m2), ldm, N, K, _ptr(s24), _nbytes(s24, "s24"),
-                                            _ptr(mask_r), K, _stream(stream)))
+                                            _ptr(mask_r), K, _stream()))
     return s24, mask_r
 
 
@@ -764,8 +788,9 @@ def spw_spmm24_plan(hdr_r, M: int, sm_count: int = 0) -> dict:
     return {name: getattr(info, name) for name, _ in info._fields_}
 
 
+@_on_stream
 def spw_spmm24(hdr_r, buf_r: torch.Tensor, s24: torch.Tensor, X: torch.Tensor,
-               Y: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+               Y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
     """Prefill on the 2:4 + residual split: Y = X . (S + R)^T, S on sparse tensor cores."""
     h = _hdr(hdr_r)
     X2, ldx = _rows(_half(X, "X"), "X")
@@ -781,7 +806,7 @@ def spw_spmm24(hdr_r, buf_r: torch.Tensor, s24: torch.Tensor, X: torch.Tensor,
         ws = torch.zeros(need, dtype=torch.uint8, device=X.device)
     _check("spw_spmm24", lib().spw_spmm24(
         ctypes.byref(h), _ptr(buf_r), _ptr(s24), _nbytes(s24, "s24"), _ptr(X2), M, ldx, _ptr(Y2), ldy,
-        _ptr(ws), _nbytes(ws), _stream(stream)))
+        _ptr(ws), _nbytes(ws), _stream()))
     return Y
 
 
@@ -811,23 +836,6 @@ def _whole(**tensors):
     for name, t in tensors.items():
         if t is not None and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-
-
-def _on_stream(fn):
-    """Gives a call its `stream` argument (by keyword, or after all others).  The call runs with
-    that stream current, so that what it allocates belongs to the stream that uses it, and what it
-    clears is cleared there."""
-    n = fn.__code__.co_argcount
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if len(args) == n + 1:
-            args, stream = args[:n], args[n]
-        if stream is None:
-            return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-    return call
 
 
 def _mat(t: torch.Tensor, rows: int | None, cols: int, name: str) -> tuple[torch.Tensor, int, int]:
