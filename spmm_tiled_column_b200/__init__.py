@@ -694,10 +694,19 @@ def spw_spmv_ffn(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor,
     return h, act_bits
 
 
+_timeouts = 0  # timeouts reported so far: the holders' workspaces from before the last are void
+
+
 def spw_last_device_status(stream=None) -> int:
+    """Synchronise the stream, then read and clear the device status word (see include/spw.h).
+    After SPW_ERR_TIMEOUT the split counters of a decode workspace are undefined: the holders below
+    replace theirs at their next call; a caller's own has to be zeroed."""
+    global _timeouts
     code = ctypes.c_int()
     _check("spw_last_device_status", lib().spw_last_device_status(_stream(stream),
                                                                   ctypes.byref(code)))
+    if code.value == SPW_ERR_TIMEOUT:
+        _timeouts += 1
     return code.value
 
 
@@ -706,7 +715,9 @@ class DecodeGroup:
 
     The header array, weight pointers and workspace are built once; each call only
     refreshes the input and output pointers and leading dimensions, so the per-call host
-    cost is one library call (serving loops that decode the same layers every step)."""
+    cost is one library call (serving loops that decode the same layers every step).  Its
+    workspace `ws` is one for all calls: they must not overlap, and after a reported timeout
+    it has to be zeroed."""
 
     def __init__(self, hdrs, bufs, B: int, ws: torch.Tensor | None = None):
         self.n = len(hdrs)
@@ -1088,15 +1099,18 @@ class _Workspaces:
     """A holder's zeroed decode workspaces: one for each kind of call, batch and stream, so that
     calls on two streams can overlap.  A captured call gets its own (cleared by the graph): one
     that the graph shared with eager calls or with another graph would be in use twice when they
-    run at once, and before the first replay it would not be cleared."""
+    run at once, and before the first replay it would not be cleared.  After a reported timeout,
+    which leaves counters undefined, all are made anew."""
 
     def __init__(self, device):
-        self._device, self._held = device, {}
+        self._device, self._held, self._timeouts = device, {}, _timeouts
 
     def get(self, kind: str, B: int, size) -> torch.Tensor | None:
         """For a call on the current stream; size() gives the bytes (None for 0)."""
         if torch.cuda.is_current_stream_capturing():
             return self._new(size())
+        if self._timeouts != _timeouts:
+            self._held, self._timeouts = {}, _timeouts
         key = kind, B, _stream().value
         if key not in self._held:
             self._held[key] = self._new(size())

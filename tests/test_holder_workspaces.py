@@ -93,3 +93,23 @@ def test_stream_as_the_last_positional_argument(world, kind):
     args = (0.0, None, None, 0, None, None) if kind == "ep" else (0.0, None, None)
     call(torch.empty(1, K), *args, 7)
     assert world.calls[0][1:] == (7, 7)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_made_anew_after_a_reported_timeout(world, kind, monkeypatch):
+    class Library:
+        code = spw.SPW_OK
+
+        def spw_last_device_status(self, stream, at):
+            at._obj.value = self.code
+            return spw.SPW_OK
+    library = Library()
+    monkeypatch.setattr(spw, "lib", lambda: library)
+    call = call_of(kind)
+    x = torch.empty(1, K)
+    for library.code in (spw.SPW_OK, spw.SPW_ERR_FORMAT, spw.SPW_ERR_TIMEOUT, spw.SPW_OK):
+        call(x, stream=1), call(x, stream=2)
+        assert spw.spw_last_device_status() == library.code
+    call(x, stream=1), call(x, stream=2)
+    ws = [id(t) for t, _, _ in world.calls]
+    assert ws[0:2] == ws[2:4] == ws[4:6] and ws[6:8] == ws[8:10] and len(set(ws)) == 4
