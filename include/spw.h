@@ -554,7 +554,8 @@ int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_f
  *   dV_gate, dV_up: dG^T X and dU^T X at the kept positions.
  * The gradient of a kept weight stands where the weight stands in the TCB values section:
  * dV has (bytes_total - off_values) / 2 fp16 entries (layout above; the filling of a tile
- * is written as zeros), so an optimiser can update the section in place.
+ * is written as zeros, and so are the entries of a tile that disagrees with its header), so an
+ * optimiser can update the section in place.
  *   d_dX may be NULL, and d_dV_gate and d_dV_up (both, and then d_X too); not all of them.
  *   dX and dV must not overlap any input.  ReLU's slope at 0 is 0.
  * fp32 sums, one rounding to fp16 of each result; a dG, dU or result beyond fp16 becomes

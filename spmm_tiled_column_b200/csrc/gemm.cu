@@ -362,6 +362,22 @@ __device__ inline void store_block(float* stage, int lane, uint16_t* Y, int ldy,
     }
 }
 
+// A tile whose bitmaps and pointers disagree counts as empty: zeros over what it claims, or, where
+// that is no tile's size or leaves the section, over its bitmaps' number of units behind its start
+// and before its end (one of the two pointers may be right).
+__device__ __noinline__ void zero_disagreeing(uint16_t* dv, uint64_t section, uint32_t u0, uint32_t u1, uint32_t n, int lane) {
+    auto zero = [&](uint64_t first, uint64_t count) {
+        if (first + count > section) return;
+        for (uint64_t i = lane; i < count; i += 32) ((uint4*)dv)[first + i] = make_uint4(0u, 0u, 0u, 0u);
+    };
+    if (u1 >= u0 && u1 <= section && u1 - u0 <= kStripRows * kTileCols / 8) {
+        zero(u0, u1 - u0);
+    } else {
+        zero(u0, n);
+        if (u1 >= n) zero(u1 - n, n);
+    }
+}
+
 template <int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUtensorMap ta1,
@@ -636,13 +652,13 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                     float v[32];
                     const int kt = (w.nt * p.BN + c) / kTileCols;
                     const bool in = strip < p.n_strips && kt < p.n_ktiles;  // warp-uniform
-                    uint32_t lo0 = 0, lo1 = 0, hi0 = 0, hi1 = 0, u0 = 0;
+                    uint32_t lo0 = 0, lo1 = 0, hi0 = 0, hi1 = 0, u0 = 0, u1 = 0;
                     int s0 = 0, s1 = 0, total = 0;
                     bool fits = false;
                     if (in) {
                         const size_t t = (size_t)strip * p.n_ktiles + kt;
                         u0 = __ldg(p.tileptr[w.prob] + t);
-                        const uint32_t u1 = __ldg(p.tileptr[w.prob] + t + 1);
+                        u1 = __ldg(p.tileptr[w.prob] + t + 1);
                         const uint4 bw = __ldg((const uint4*)(p.bitmaps[w.prob] + t * kTileCols) + lane);
                         lo0 = bw.x; hi0 = bw.y; lo1 = bw.z; hi1 = bw.w;  // columns 2l, 2l+1
                         const int c0 = __popc(lo0) + __popc(hi0), c1 = __popc(lo1) + __popc(hi1);
@@ -651,7 +667,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
                         s0 = incl - c0 - c1;
                         s1 = s0 + c0;
                         fits = u1 >= u0 && u1 <= p.values_units[w.prob] && (uint32_t)(total + 7) / 8u == u1 - u0;
-                        if (!fits && lane == 0) raise_status(p.status, SPW_ERR_FORMAT);
+                        if (!fits) {
+                            if (lane == 0) raise_status(p.status, SPW_ERR_FORMAT);
+                            if (!hi) zero_disagreeing(p.dv[w.prob], p.values_units[w.prob], u0, u1, (uint32_t)(total + 7) / 8u, lane);
+                        }
                     }
                     uint16_t* out = p.dv[w.prob] + (size_t)u0 * 8;
                     // the warp's words and the place of its first kept row in each column
