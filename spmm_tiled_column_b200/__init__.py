@@ -208,24 +208,25 @@ def _rows(t: torch.Tensor, name: str) -> tuple[torch.Tensor, int]:
         t = t.unsqueeze(0)
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
-    return t, _ld(t, name)
+    return t, _ld(t.stride(0), t.shape[0], t.shape[1], name)
 
 
 _INT_MAX = 2 ** 31 - 1
 
 
-def _ld(t: torch.Tensor, name: str) -> int:
-    """Leading dimension of a 2-D view with unit column stride.  The library steps from row to
-    row by it, so rows that overlap (a broadcast, a sliding window) cannot be handed over."""
-    m, n = t.shape
-    ld = t.stride(0)
-    if m > 1 and ld < n:
+def _ld(ld: int, m: int, n: int, name: str) -> int:
+    """Leading dimension of an m x n view with rows ld elements apart and unit column stride.  The
+    library steps from row to row by it, so rows that overlap (a broadcast, a sliding window)
+    cannot be handed over; M and ld are C ints, and ctypes would cut longer numbers to 32 bits."""
+    if m <= 1:  # any stride
+        return n if ld > _INT_MAX else max(ld, n)
+    if n <= ld <= _INT_MAX and m <= _INT_MAX:
+        return ld
+    if ld < n:
         raise ValueError(f"{name} is {m} x {n} with rows {ld} elements apart: they overlap "
                          "(make it contiguous)")
-    if m > 1 and max(m, ld) > _INT_MAX:  # M and ld are C ints, and ctypes cuts to 32 bits
-        raise ValueError(f"{name} is {m} x {n} with rows {ld} elements apart: the library counts both "
-                         f"up to {_INT_MAX}")
-    return n if ld > _INT_MAX else max(ld, n)  # (a single row: any stride)
+    raise ValueError(f"{name} is {m} x {n} with rows {ld} elements apart: the library counts both "
+                     f"up to {_INT_MAX}")
 
 
 def _need(t: torch.Tensor, rows: int, cols: int, name: str):
@@ -841,11 +842,12 @@ def _same_device(*tensors):
                              f"device is cuda:{dev}")
 
 
-def _whole(**tensors):
+def _whole(names: str, *tensors):
     """Raw buffers go over as a pointer and a number of bytes, so a tensor with gaps or repeats
     (whose storage holds other or fewer bytes than its size says) cannot."""
-    for name, t in tensors.items():
+    for t in tensors:
         if t is not None and not t.is_contiguous():
+            name = names.split()[[u is t for u in tensors].index(True)]
             raise ValueError(f"{name} must be contiguous")
 
 
@@ -862,7 +864,7 @@ def _mat(t: torch.Tensor, rows: int | None, cols: int, name: str) -> tuple[torch
     if n != cols or (rows is not None and m != rows):
         raise ValueError(f"{name} is {m} x {n}; the call takes {'any' if rows is None else rows} rows of "
                          f"{cols} columns")
-    return t, m, _ld(t, name)
+    return t, m, _ld(t.stride(0), m, n, name)
 
 
 def _out(t: torch.Tensor | None, rows: int, cols: int, like: torch.Tensor, name: str):
@@ -939,7 +941,7 @@ def spw_spmv_ep(hdr, buf: torch.Tensor, x: torch.Tensor, threshold: float = 0.0,
     h = _hdr(hdr)
     x2, B, ldx = _mat(x, None, h.K, "x")
     _same_device(x, buf, act_bits, bias, residual, y, ws)
-    _whole(buf=buf, act_bits=act_bits, ws=ws)
+    _whole("buf act_bits ws", buf, act_bits, ws)
     ep = _epilogue(bias, act, residual, B, h.N)
     _need_buf(buf, h)
     _need_words(act_bits, h.K)
@@ -969,7 +971,7 @@ def spw_spmm_ep(hdr, buf: torch.Tensor, X: torch.Tensor, bias: torch.Tensor | No
     h = _hdr(hdr)
     X2, M, ldx = _mat(X, None, h.K, "X")
     _same_device(X, buf, bias, residual, Y, ws)
-    _whole(buf=buf, ws=ws)
+    _whole("buf ws", buf, ws)
     ep = _epilogue(bias, act, residual, M, h.N)
     _need_buf(buf, h)
     Y, pY, ldy = _out(Y, M, h.N, X, "Y")
@@ -1000,7 +1002,7 @@ def spw_spmm_ffn(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torch.Tensor,
         raise ValueError("G and U go together")
     save = save or G is not None
     _same_device(X, buf_gate, buf_up, H, G, U, ws)
-    _whole(buf_gate=buf_gate, buf_up=buf_up, ws=ws)
+    _whole("buf_gate buf_up ws", buf_gate, buf_up, ws)
     _need_buf(buf_gate, hg, "buf_gate")
     _need_buf(buf_up, hu, "buf_up")
     H, pH, ldh = _out(H, M, hg.N, X, "H")
@@ -1043,7 +1045,7 @@ def spw_spmm_ffn_backward(hdr_gate, buf_gate: torch.Tensor, hdr_up, buf_up: torc
         X2, _, ldx = _mat(X, M, hg.K, "X")
         pX = X2.data_ptr()
     _same_device(G, U, dH, X, buf_gate, buf_up, dX, dV_gate, dV_up, ws)
-    _whole(buf_gate=buf_gate, buf_up=buf_up, ws=ws)
+    _whole("buf_gate buf_up ws", buf_gate, buf_up, ws)
     _need_buf(buf_gate, hg, "buf_gate")
     _need_buf(buf_up, hu, "buf_up")
     pdX, lddx = None, 0
@@ -1080,7 +1082,7 @@ def spw_spmm_backward(hdr, buf: torch.Tensor, X: torch.Tensor | None, dY: torch.
         X2, _, ldx = _mat(X, M, h.K, "X")
         pX = X2.data_ptr()
     _same_device(dY, X, buf, dX, dV, ws)
-    _whole(buf=buf, ws=ws)
+    _whole("buf ws", buf, ws)
     _need_buf(buf, h)
     pdX, lddx = None, 0
     if need_dx:

@@ -52,4 +52,4 @@ def test_column_set_with_gaps_is_refused(call):
 
 
 def test_contiguous_buffers_pass_the_check():
-    spw._whole(ws=None, buf=torch.zeros(64, dtype=torch.uint8)[16:48])
+    spw._whole("ws buf", None, torch.zeros(64, dtype=torch.uint8)[16:48])
