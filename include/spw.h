@@ -115,7 +115,9 @@ int spw_version(void);
  * workspace are only touched after the previous kernel has completed, so chaining
  * layers stays correct; the one requirement is that the kernel immediately before
  * spw_spmv on the stream does not write the TCB buffer being read (true for weights
- * compressed at load time and left alone).  Returns the previous setting. */
+ * compressed at load time and left alone; after an update of the values section in place,
+ * a kernel that is no overlapped decode, or a synchronisation, has to come first).  Returns the previous
+ * setting. */
 int spw_set_launch_overlap(int enable);
 
 /* Column fetch for the CUDA-core decode (process-wide; mode 0 by default).  With a column
@@ -500,9 +502,11 @@ typedef struct {
 /* Decode with an epilogue, for 1 to 16 rows: the product is spw_spmv's (same arguments,
  * threshold rule and column set), the epilogue as above.  Two paths, chosen on the host by
  * shape and batch: the CUDA-core decode of spw_spmv for the fewest rows, the tensor-core
- * kernel of spw_spmm_ep with the rule applied to x from where it measured faster (3 to 6
- * rows).  On the tensor-core path a non-finite x~ entry reaches every output, also through
- * weights that the mask drops (as in spw_spmv_tc).  Deterministic.  Asynchronous.
+ * kernel of spw_spmm_ep with the rule applied to x from where it measured faster with every
+ * column on (3 to 6 rows; it decodes columns that are off as well).  On the tensor-core path a
+ * non-finite x~ entry reaches every output, also through weights that the mask drops (as in
+ * spw_spmv_tc), and a non-finite kept weight its row's outputs, also where x~ is zero.
+ * Deterministic.  Asynchronous.
  *   spw_spmv_ep_path(hdr, B): 0 (CUDA cores), 1 (tensor cores), -1 (invalid header or B).
  *   spw_spmv_ep_workspace_bytes(hdr, B): 0 on the tensor-core path (d_ws may be NULL), else
  *   spw_spmv's workspace with its rules (counters zero before the first call, left zero).

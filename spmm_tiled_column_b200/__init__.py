@@ -1189,7 +1189,9 @@ class SparseLinear:
 
     def values(self) -> torch.Tensor:
         """The kept weights as they stand in the buffer (fp16 view of the values section, the
-        order of a packed gradient; a tile's filling must stay zero)."""
+        order of a packed gradient; a tile's filling must stay zero).  With launch overlap on
+        (spw_set_launch_overlap) a kernel other than a decode, or a synchronisation, has to come
+        between one that writes here and a decode of this layer."""
         return self.buf[self.hdr.off_values:self.hdr.bytes_total].view(torch.float16)
 
     def decompress(self, out=None, stream=None):

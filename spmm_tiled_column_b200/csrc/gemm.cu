@@ -743,8 +743,10 @@ gemm_kernel(const __grid_constant__ CUtensorMap ta0, const __grid_constant__ CUt
 
 // ------------------------------------------------------------------ dG and dU
 // dG = dH U act'(G), dU = dH act(G) (M x ld, ld = N rounded up to 8; the columns past N are
-// not written and not read), 8 columns per thread; clears the products' counters as well.  Memory-bound: 10 bytes an entry.  Rounded
-// to fp16 because they are operands of the products that follow; an overflow becomes an
+// not written and not read), 8 columns per thread; clears the products' counters as well.
+// Memory-bound: 10 bytes an entry.  Rounded to fp16 because they are operands of the products
+// that follow (the gradients' relative error against 64 bits is 2.9e-4, 2.1e-4 of it the rounding of
+// the result; keeping the remainders would double the products); an overflow becomes an
 // infinity there, which a loss scaler looks for.
 __global__ void __launch_bounds__(256)
 gate_grad_kernel(const uint16_t* __restrict__ G, int ldg, const uint16_t* __restrict__ U, int ldu,

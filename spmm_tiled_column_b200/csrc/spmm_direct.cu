@@ -7,8 +7,9 @@
 //   kDecode  as kEp for at most 16 rows, with the decode's threshold rule or column set
 //
 // With few tokens each weight tile is needed once or twice, so what bounds the product is the
-// decoding (about 900 warp instructions and 400 shared-memory wavefronts for a 64 x 64 tile, of
-// which an SM does two in 0.58 us) and, for small weights, the latency of the chain pointers ->
+// decoding (for a 64 x 64 tile about 900 warp instructions and, the exchange of the pieces
+// included, 507 shared-memory wavefronts: 11008 x 4096 at 128 tokens; an SM does two tiles in
+// 0.58 us) and, for small weights, the latency of the chain pointers ->
 // compressed tile -> decode -> MMA -> result (6.3 us for one tile).  At 50 %: 4096 x 4096 with an
 // epilogue 16.2 us at 16 tokens, 19.2 at 128; 4096 x 11008 32 and 36; 11008 x 4096 gated 66 and 77.
 // The design follows from that:

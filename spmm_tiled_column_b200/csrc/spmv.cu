@@ -1310,6 +1310,9 @@ int spw_spmv_ep_path(const spw_format* hdr, int B) {
     // last warp adds up row by row; the tensor cores' hardly does.  Measured at 50 % (us, 1 / 4 /
     // 8 rows, against tensor cores): 1000 x 1000 6.9 / 9.9 / 14 against 7.9; 512 x 8192 10 / 20 /
     // 38 against 16; 4096 x 4096 11 / 18 / 30 against 16; 11008 x 4096 19 / 28 / 44 against 34.
+    // Measured with every column on, and blind to the rule: columns that are off cost these cores
+    // nothing, the tensor cores their decode (4096 x 11008, 4 rows, half the columns off: 30.8
+    // against 36.8; 6 rows 40.9 against 38.4).  2368: warps of the decode's grid on 148 SMs.
     const double entries = 1e-6 * (double)hdr->N * hdr->K;
     double pieces = 2368.0 / hdr->n_strips;
     if (pieces > hdr->n_ktiles) pieces = hdr->n_ktiles;
