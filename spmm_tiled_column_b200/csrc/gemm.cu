@@ -145,7 +145,7 @@ constexpr int kSmemLimit = 227 * 1024;
 
 struct GemmParams {
     int m_tiles, n_tiles, group_m, problem_tiles;
-    int n_units, n_whole, parts;
+    int n_units, parts;
     int ksteps, kseg;  // reduction blocks of 64 of a tile; those of its first segment (kDx)
     int BN, stages;
     uint32_t block_bytes, stage_bytes, off_bar;  // this CTA's operands, 64 deep; kStageBlocks of them
@@ -178,10 +178,9 @@ __device__ inline Unit unit_of(const GemmParams& p, int u) {
     w.part = 0;
     w.k0 = 0;
     w.k1 = p.ksteps;
-    if (u >= p.n_whole) {
-        w.stile = (u - p.n_whole) / p.parts;
-        w.part = (u - p.n_whole) - w.stile * p.parts;
-        tile = p.n_whole + w.stile;
+    if (p.parts > 1) {
+        tile = w.stile = u / p.parts;
+        w.part = u - tile * p.parts;
         w.k0 = (int)((long long)w.part * p.ksteps / p.parts);
         w.k1 = (int)((long long)(w.part + 1) * p.ksteps / p.parts);
     }
@@ -222,18 +221,6 @@ __device__ inline uint64_t umma_desc_mn_sw128(uint32_t saddr) {
     d |= (uint64_t)(1024 >> 4) << 32;
     d |= (uint64_t)1 << 46;
     d |= (uint64_t)2 << 61;
-    return d;
-}
-
-// No swizzle: core matrices of 8 rows x 16 bytes, 128 contiguous bytes each; lbo and sbo are
-// the strides between them along K and along M or N (K-major), or the other way round
-// (MN-major: a core matrix is then 8 K rows of 8 M or N elements).
-__device__ inline uint64_t umma_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-    d |= (uint64_t)(lbo >> 4) << 16;
-    d |= (uint64_t)(sbo >> 4) << 32;
-    d |= (uint64_t)1 << 46;
     return d;
 }
 
@@ -832,7 +819,7 @@ int gemm_pairs() {
 }
 
 struct GemmPlan {
-    int m_tiles, n_tiles, problems, BN, parts, n_whole, stages;
+    int m_tiles, n_tiles, problems, BN, parts, stages;
     long long tiles, n_units;
     uint32_t block_bytes, stage_bytes, off_bar, off_stage;
     size_t smem;
@@ -868,9 +855,8 @@ int plan_gemm(long long rows, long long cols, int problems, long long ksteps, in
     }
     if (g->tiles * g->parts > 0x3fffffffll) return SPW_ERR_UNSUPPORTED;
     g->cost = best;
-    g->n_whole = g->parts > 1 ? 0 : (int)g->tiles;
-    const long long split = g->tiles - g->n_whole;
-    g->n_units = g->n_whole + split * g->parts;
+    const long long split = g->parts > 1 ? g->tiles : 0;
+    g->n_units = g->tiles * g->parts;
     g->counter_bytes = round_up_u64(8ull * (uint64_t)split, 256);
     g->partial_bytes = 4ull * (uint64_t)split * g->parts * 2 * g->BN * kCtaRows;
     g->block_bytes = kABytes + (uint32_t)g->BN / 2 * 128;
@@ -892,7 +878,6 @@ void fill_params(const GemmPlan& g, long long ksteps, GemmParams* p) {
     p->group_m = g.m_tiles < 16 ? g.m_tiles : 16;
     p->problem_tiles = g.m_tiles * g.n_tiles;
     p->n_units = (int)g.n_units;
-    p->n_whole = g.n_whole;
     p->parts = g.parts;
     p->ksteps = p->kseg = (int)ksteps;
     p->BN = g.BN;

@@ -78,15 +78,6 @@ struct DirectParams {
     uint32_t t_bits;  // magnitude bits of the smallest fp16 not below the threshold, at least 1
 };
 
-__device__ inline uint64_t desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
-    d |= (uint64_t)(lbo >> 4) << 16;
-    d |= (uint64_t)(sbo >> 4) << 32;
-    d |= (uint64_t)1 << 46;
-    return d;
-}
-
 __device__ inline float4 ld_cluster_f4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -312,7 +303,7 @@ direct_kernel(const __grid_constant__ CUtensorMap tx0, const __grid_constant__ C
         const uint32_t idesc = idesc_f16(128, tok) | (MODE == kDx ? 1u << 15 : 0u);
         // the same operand bytes, 16 of the reduction a slice
         constexpr uint32_t kSliceA = MODE == kDx ? 256u : 4096u;
-        const uint64_t ad0 = MODE == kDx ? desc_plain(sbase + p.off_w, 128, 1024) : desc_plain(sbase + p.off_w, 2048, 128);
+        const uint64_t ad0 = MODE == kDx ? umma_desc_plain(sbase + p.off_w, 128, 1024) : umma_desc_plain(sbase + p.off_w, 2048, 128);
         const uint64_t bd0 = umma_desc_sw128(sbase);
         uint32_t xo = 0, wo = 0;  // the slots' offsets
         for (int n = 0; n < nk; n++) {

@@ -65,6 +65,18 @@ __device__ inline void tmem_cp_128x128b(uint32_t taddr, uint32_t saddr) {
     asm volatile("tcgen05.cp.cta_group::1.128x128b [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
 }
 
+// No swizzle: core matrices of 8 rows x 16 bytes, 128 contiguous bytes each; lbo and sbo are
+// the strides between them along K and along M or N (K-major), or the other way round
+// (MN-major: a core matrix is then 8 K rows of 8 M or N elements).
+__device__ inline uint64_t umma_desc_plain(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFF);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(sbo >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    return d;
+}
+
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
