@@ -563,8 +563,9 @@ int spw_spmm_ffn(const spw_format* hdr_gate, const void* d_buf_gate, const spw_f
  *   d_dX may be NULL, and d_dV_gate and d_dV_up (both, and then d_X too); not all of them.
  *   dX and dV must not overlap any input.  ReLU's slope at 0 is 0.
  * fp32 sums, one rounding to fp16 of each result; a dG, dU or result beyond fp16 becomes
- * an infinity, which a loss scaler looks for.  M == 0 writes zeros to dV.  Workspace and
- * errors as spw_spmm_ep (both weights expanded, dG and dU). */
+ * an infinity, which a loss scaler looks for (one in dG or dU spreads, as Inf or NaN, over
+ * its token's row of dX and its weight row's entries of dV, and no further).  M == 0 writes
+ * zeros to dV.  Workspace and errors as spw_spmm_ep (both weights expanded, dG and dU). */
 uint64_t spw_spmm_ffn_backward_workspace_bytes(const spw_format* hdr_gate, const spw_format* hdr_up,
                                                int M);
 int spw_spmm_ffn_backward(const spw_format* hdr_gate, const void* d_buf_gate,
